@@ -285,6 +285,112 @@ int svdq_quantize_weights_noalloc(const uint16_t* W, const uint16_t* smooth, con
                                   int N, int K, uint8_t* qweight, uint8_t* wscales,
                                   uint16_t* wcscales, uint16_t* wtscale, void* stream);
 
+/* ---- between the linears of a block --------------------------------------
+ *
+ * What stands between the linears of a transformer block (the pages' own
+ * description ends at the linears): the norms with the block's gate and
+ * residual scale, rotary positions on q and k, and the attention.  Common to
+ * the three calls:
+ * - dtype: SVDQ_BF16 or SVDQ_FP16, the type of every 16-bit tensor of the
+ *   call; arithmetic is fp32, results are rounded once (nearest-even).
+ * - Sequences: rows of several sequences stand behind one another; sequence
+ *   s has the rows [cu_seqlens[s], cu_seqlens[s + 1]).  cu_seqlens is an
+ *   int32 array [n_seqs + 1] in DEVICE memory, not decreasing, within
+ *   [0, T]; NULL (with n_seqs = 1): one sequence of all T rows.  Sequences
+ *   may be empty.  Rows in no sequence are not read for a result and their
+ *   outputs stay as they were.  The array is not checked on the host; the
+ *   kernels stay inside the tensors whatever it holds.
+ * - Strides are in elements, multiples of 8; 16-bit tensors are 16-byte
+ *   aligned.  The stride of a dimension of size one is not used.
+ * - T = 0 returns SVDQ_OK and enqueues nothing.
+ * - No workspace: calls on several streams, and captured calls, share
+ *   nothing but their own tensors.
+ * - Outputs that meet inputs in memory give SVDQ_ERR_INVALID_ARG, unless a
+ *   call says otherwise.  (Decided from the addresses and strides: operands
+ *   side by side in the rows of one buffer are recognised as apart; two
+ *   interleaved operands of different row strides count as meeting.) */
+#define SVDQ_BF16 0
+#define SVDQ_FP16 1
+#define SVDQ_NORM_NONE 0
+#define SVDQ_NORM_RMS 1
+#define SVDQ_NORM_LAYER 2
+#define SVDQ_GATE_NONE 0
+#define SVDQ_GATE_LINEAR 1
+#define SVDQ_GATE_TANH 2
+
+/* The norms before and after a block with its gate and residual scale, one
+ * pass: for every row t, in sequence s,
+ *   u = post(y_t)
+ *   h_t = residual_scale * x_t + g_s * u
+ *   n_t = pre(h_t) * (1 + scale_s) + shift_s
+ * rms(v) = v / sqrt(mean(v^2) + eps) * weight, layer(v) = (v - mean) /
+ * sqrt(var + eps) * weight, g_s = gate_s (SVDQ_GATE_LINEAR), tanh(gate_s)
+ * (SVDQ_GATE_TANH) or 1; n is taken from h before its rounding.
+ *   x [T, ldx], y [T, ldy]     residual stream and the branch's output; y may
+ *                 be NULL (the first norm of a stack): then h must be NULL,
+ *                 post and gate none and residual_scale 1, and h is x.
+ *   post, pre     SVDQ_NORM_*; post_weight, pre_weight [C] or NULL (1).
+ *   gate, scale, shift   [n_seqs, ld] or NULL (1, 0, 0); ld may be 0 (one row
+ *                 for all) and the three may be views of one tensor.
+ *   h [T, ldh]    out;  n [T, ldn] out, or NULL (then pre, scale and shift
+ *                 none): only h.
+ * h and n may each be exactly x or y (same address and stride).
+ * Limits: C % 8 == 0, C <= 8192 (else SVDQ_ERR_UNSUPPORTED). */
+int svdq_norm_gate_residual(int dtype, const uint16_t* x, int64_t ldx, const uint16_t* y,
+                            int64_t ldy, int T, int C, const int32_t* cu_seqlens, int n_seqs,
+                            int post, const uint16_t* post_weight, int gate_kind,
+                            const uint16_t* gate, int64_t ld_gate, float residual_scale, int pre,
+                            const uint16_t* pre_weight, const uint16_t* scale, int64_t ld_scale,
+                            const uint16_t* shift, int64_t ld_shift, float eps, uint16_t* h,
+                            int64_t ldh, uint16_t* n, int64_t ldn, void* stream);
+
+/* Frequencies of svdq_rope_qk: turns[p] = theta^(-2 i / axes[a]) / (2 pi) for
+ * pair p, the i-th of axis a (axes one behind the other).  axes and turns are
+ * HOST arrays, turns [sum(axes) / 2]; no device work.  A caller with
+ * frequencies of its own fills turns itself. */
+int svdq_rope_turns(const int* axes, int n_axes, double theta, double* turns);
+
+/* Rotary positions with several axes (time, height, width, ...) on q and k,
+ * after their per-head RMS norm where a weight is given:
+ *   v = q_t,h / sqrt(mean(q_t,h^2) + eps) * q_weight      (k likewise)
+ *   phi = 2 pi positions[t, a] turns[p]                   (pair p of axis a)
+ *   (e0, e1) -> (e0 cos phi - e1 sin phi, e0 sin phi + e1 cos phi)
+ * Pair p is (2p, 2p + 1) (interleaved), or (p, p + R / 2), R = sum(axes);
+ * elements from R on keep v.
+ *   q [T, Hq, D], k [T, Hk, D]   by strides (token, head); either may be
+ *                 absent (heads 0, pointers NULL).
+ *   positions     [T, ld_pos] int32, device, n_axes columns used, any value
+ *                 (angles are taken in 64 bits).
+ *   axes, turns   HOST arrays [n_axes] (even widths) and [R / 2], read during
+ *                 the call.
+ *   q_weight, k_weight   [D] or NULL: no norm for that tensor.
+ *   q_out, k_out  out, same shapes; each may be exactly its input.
+ * Limits: n_axes <= 4, D % 8 == 0, D <= 256, R <= D, and R % 16 == 0 without
+ * interleaving (else SVDQ_ERR_UNSUPPORTED). */
+int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, int Hq,
+                 const uint16_t* k, int64_t k_stride_t, int64_t k_stride_h, int Hk, int T, int D,
+                 const int32_t* positions, int64_t ld_pos, const int* axes, int n_axes,
+                 const double* turns, int interleaved, const uint16_t* q_weight,
+                 const uint16_t* k_weight, float eps, uint16_t* q_out, int64_t qo_stride_t,
+                 int64_t qo_stride_h, uint16_t* k_out, int64_t ko_stride_t, int64_t ko_stride_h,
+                 void* stream);
+
+/* Attention over whole packed sequences: for row i of a sequence of L,
+ *   out_i = sum_j softmax_j(scale * q_i . k_j) v_j,
+ * j over all L rows (causal = 0) or j <= i; query head h uses key / value
+ * head h / (Hq / Hk).  Scores, softmax and sums in fp32; the weights are
+ * rounded to the tensors' type for the product with v.  Keys and values that
+ * a row does not attend, whatever they hold (inf, NaN), do not reach it.
+ *   q [T, Hq, D], k, v [T, Hk, D], out [T, Hq, D]  by strides (token, head).
+ *   scale         finite and positive (usually 1 / sqrt(D)).
+ * Limits: Hq % Hk == 0, D % 8 == 0, D <= 128 (else SVDQ_ERR_SHAPE /
+ * SVDQ_ERR_UNSUPPORTED). */
+int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h,
+                   const uint16_t* k, int64_t k_stride_t, int64_t k_stride_h, const uint16_t* v,
+                   int64_t v_stride_t, int64_t v_stride_h, int T, int Hq, int Hk, int D,
+                   const int32_t* cu_seqlens, int n_seqs, int causal, float scale, uint16_t* out,
+                   int64_t o_stride_t, int64_t o_stride_h, void* stream);
+
 /* ---- helpers ------------------------------------------------------------ */
 
 /* Launch shape svdq_quantize_act uses on the current device for an [M, K]

@@ -24,7 +24,7 @@ LIB = os.path.join(HERE, "libsvdq.so")
 SOURCES = ["svdq.cu"]
 HEADERS = ["sm100_ptx.cuh", "kq_quantize_act.cuh", "kg_w4a4_linear.cuh",
            "kg2_w4a4_linear_pair.cuh", "ks_w4a4_linear_small.cuh", "kr_scales.cuh",
-           "kw_quantize_weights.cuh"]
+           "kw_quantize_weights.cuh", "kn_norm_gate.cuh", "kp_rope_qk.cuh", "ka_attention.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

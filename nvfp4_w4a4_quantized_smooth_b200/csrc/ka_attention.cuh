@@ -1,0 +1,580 @@
+// ka_attention.cuh -- attention over whole packed sequences:
+//
+//   out_i = sum_j w_ij v_j,  w_ij = softmax_j(scale q_i . k_j),
+//
+// j over the keys of row i's sequence (full), or over j <= i (causal); query
+// head h reads key / value head h / (Hq / Hk).
+//
+// One work item is 256 query rows of one head (two slots of 128 rows, the
+// tensor core's row count) against all key tiles of 128 they attend.  Per
+// key tile and slot: S = Q K^T into TMEM (fp32), one softmax step by the
+// slot's four warps (one thread per row, so no shuffles), P back into the
+// same TMEM columns as 16-bit values, O += P V with P read from TMEM.  While
+// one slot's warps work on their tile the tensor core runs the other slot's
+// products, and K and V tiles pass both slots from one ring in shared memory.
+//
+// The softmax keeps a running reference m (log2 units after the scale), sum
+// and O relative to it.  O is rescaled only when a row's maximum has grown by
+// more than 2^8 over its reference: until then the exponentials stay below
+// 2^8, which neither the fp32 sums nor the 16-bit P lose digits over (P's
+// relative rounding is the same at every exponent, fp16's range is 65504).
+// P is rounded to the input type for the tensor core (half a step, 2^-9 of
+// each weight for bf16); the sum is over the unrounded fp32 weights.
+//
+// Keys that a row does not attend are replaced by -inf after the product, by
+// selection, so what they hold does not matter.  Values need more, since a
+// zero weight times inf or NaN is NaN: the tile behind a sequence's end
+// holds other rows, and on the causal diagonal a tile holds values that some
+// of its rows do not attend.  For these tiles alone two guard warps zero the
+// rows behind the end (only up to the next multiple of 16; the product stops
+// there) and, when causal, replace non-finite values by zero and note their
+// keys; the epilogue adds a noted value back into the rows that do attend it.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "kn_norm_gate.cuh"
+#include "sm100_ptx.cuh"
+
+namespace svdq {
+namespace ka {
+
+constexpr int ROWS = 128;               // query rows of a slot, keys of a tile
+constexpr int ITEM_ROWS = 2 * ROWS;     // query rows of a work item
+constexpr int MAX_D = 128;
+constexpr int NUM_THREADS = 384;        // 2 x 4 softmax warps, MMA, TMA, 2 guards
+constexpr int MMA_WARP = 8, TMA_WARP = 9, GUARD_WARP = 10;
+constexpr uint32_t BOX_BYTES = ROWS * 128;   // 128 rows x 64 elements, 128-byte swizzle
+constexpr uint32_t TMEM_COLS = 512;
+constexpr uint32_t TM_S = 0;            // S / P of slot s at 128 s
+constexpr uint32_t TM_O = 256;          // O of slot s at 256 + 128 s
+constexpr float RESCALE_LOG2 = 8.f;
+// Registers per thread of the softmax warps and of the others.
+constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 80;
+
+// NB: 64-element boxes per row (1: D <= 64, 2: D <= 128).
+template <int NB>
+struct Shape {
+  static constexpr uint32_t TILE_BYTES = NB * BOX_BYTES;
+  static constexpr int STAGES = NB == 2 ? 5 : 10;
+  static constexpr uint32_t OFF_Q = 0;
+  static constexpr uint32_t OFF_KV = 2 * TILE_BYTES;
+  static constexpr uint32_t OFF_BAR = OFF_KV + STAGES * TILE_BYTES;
+  // full, empty, guard_go, guard_done [STAGES], q_full, q_empty, s_full[2],
+  // p_full[2], o_full[2], flags_full[2], flags_free[2], final
+  static constexpr int BARS = 4 * STAGES + 13;
+  // Notes of the guards, one bit per key: [item parity][guard][8 words].
+  static constexpr uint32_t OFF_FLAGS = OFF_BAR + 8 * BARS;
+  static constexpr uint32_t OFF_TMEM = OFF_FLAGS + 2 * 2 * 8 * 4;
+  static constexpr uint32_t USED = OFF_TMEM + 16;
+  static constexpr uint32_t SMEM_BYTES = USED + 1024;   // 1024-byte alignment of the boxes
+};
+static_assert(Shape<2>::SMEM_BYTES <= 232448 && Shape<1>::SMEM_BYTES <= 232448, "");
+
+constexpr uint32_t SITE_TMA_Q = 0x50, SITE_TMA_KV = 0x51, SITE_MMA_Q = 0x52, SITE_MMA_KV = 0x53,
+                   SITE_MMA_P = 0x54, SITE_MMA_GUARD = 0x55, SITE_SOFT_S = 0x56,
+                   SITE_SOFT_O = 0x57, SITE_GUARD_V = 0x58, SITE_GUARD_FLAGS = 0x59,
+                   SITE_SOFT_FLAGS = 0x5A;
+
+struct Params {
+  const int32_t* cu;        // [S + 1] or NULL: one sequence of all T rows
+  const uint16_t* v;        // for the non-finite values' way back
+  uint16_t* out;
+  int64_t vst, vsh, ost, osh;
+  int T, S, Hq, group, D;
+  int causal;
+  float scale_log2;         // scale * log2(e)
+};
+
+// One work item: rows [q0, q0 + 256) of the sequence [begin, begin + len), head h.
+struct Item {
+  int begin, len, q0, head;
+  __device__ __forceinline__ int key_tiles() const { return (len + ROWS - 1) / ROWS; }
+  // key tiles that slot s reads
+  __device__ __forceinline__ int tiles(int s, int causal) const {
+    if (q0 + s * ROWS >= len) return 0;
+    const int n = key_tiles();
+    return causal ? min(n, q0 / ROWS + s + 1) : n;
+  }
+  __device__ __forceinline__ bool guarded(int j, int causal) const {
+    return (causal && j >= q0 / ROWS) || ((j + 1) * ROWS > len && len % 16 != 0);
+  }
+};
+
+// Walks the work items of all sequences in order.  Every warp runs its own
+// copy; w must not decrease from call to call.  Offsets are clamped to
+// [0, T] and to an increasing order, so that no entry of cu can lead outside
+// the tensors.
+struct Items {
+  int s0 = 0;        // first sequence of the present group of 32
+  int64_t base = 0;  // items in front of it
+  __device__ __forceinline__ bool get(const Params& p, int64_t w, Item& it) {
+    const int lane = threadIdx.x & 31;
+    while (s0 < p.S) {
+      const int s = s0 + lane;
+      int begin = 0, len = 0;
+      if (s < p.S) {
+        begin = p.cu ? min(max(p.cu[s], 0), p.T) : 0;
+        len = (p.cu ? min(max(p.cu[s + 1], begin), p.T) : p.T) - begin;
+      }
+      const int64_t n = static_cast<int64_t>((len + ITEM_ROWS - 1) / ITEM_ROWS) * p.Hq;
+      int64_t incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+        if (lane >= o) incl += t;
+      }
+      const uint32_t mine = __ballot_sync(0xFFFFFFFFu, base + incl > w);
+      if (mine != 0u) {
+        const int src = __ffs(mine) - 1;
+        const int r = static_cast<int>(__shfl_sync(0xFFFFFFFFu, w - base - (incl - n), src));
+        it.begin = __shfl_sync(0xFFFFFFFFu, begin, src);
+        it.len = __shfl_sync(0xFFFFFFFFu, len, src);
+        const int nt = (it.len + ITEM_ROWS - 1) / ITEM_ROWS;
+        if (p.causal) {   // longest items first
+          it.head = r % p.Hq;
+          it.q0 = (nt - 1 - r / p.Hq) * ITEM_ROWS;
+        } else {          // the items of one head together: they read the same keys
+          it.head = r / nt;
+          it.q0 = (r % nt) * ITEM_ROWS;
+        }
+        return true;
+      }
+      base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+      s0 += 32;
+    }
+    return false;
+  }
+};
+
+template <int N>
+__device__ __forceinline__ void set_max_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <bool BF16>
+__device__ __forceinline__ bool is_nonfinite16(uint32_t e) {
+  constexpr uint32_t m = BF16 ? 0x7F80u : 0x7C00u;
+  return (e & m) == m;
+}
+
+template <bool BF16, int NB>
+__global__ void __launch_bounds__(NUM_THREADS, 1)
+    attention_kernel(const __grid_constant__ CUtensorMap tm_q,
+                     const __grid_constant__ CUtensorMap tm_k,
+                     const __grid_constant__ CUtensorMap tm_v, const Params p) {
+  using S_ = Shape<NB>;
+  constexpr int STAGES = S_::STAGES;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
+  const uint32_t sb = smem_u32(smem);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  auto bar = [&](int i) { return sb + S_::OFF_BAR + 8u * i; };
+  auto full_bar = [&](uint32_t s) { return bar(s); };
+  auto empty_bar = [&](uint32_t s) { return bar(STAGES + s); };
+  // A guarded value tile goes TMA -> guards -> MMA.  Both steps have a
+  // barrier per stage: a stage is not loaded again before the MMA has
+  // passed, so its phases alternate one by one, however far ahead of one
+  // another the three warps are with other stages.
+  auto guard_go = [&](uint32_t s) { return bar(2 * STAGES + s); };
+  auto guard_done = [&](uint32_t s) { return bar(3 * STAGES + s); };
+  const uint32_t q_full = bar(4 * STAGES), q_empty = bar(4 * STAGES + 1);
+  auto s_full = [&](int s) { return bar(4 * STAGES + 2 + s); };
+  auto p_full = [&](int s) { return bar(4 * STAGES + 4 + s); };
+  auto o_full = [&](int s) { return bar(4 * STAGES + 6 + s); };
+  auto flags_full = [&](int b) { return bar(4 * STAGES + 8 + b); };
+  auto flags_free = [&](int b) { return bar(4 * STAGES + 10 + b); };
+  const uint32_t final_bar = bar(4 * STAGES + 12);
+  auto s_q = [&](int s) { return sb + S_::OFF_Q + s * S_::TILE_BYTES; };
+  auto s_kv = [&](uint32_t s) { return sb + S_::OFF_KV + s * S_::TILE_BYTES; };
+  uint32_t* flags = reinterpret_cast<uint32_t*>(smem + S_::OFF_FLAGS);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+      mbar_init(guard_go(s), 1);
+      mbar_init(guard_done(s), 2);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(s_full(s), 1);
+      mbar_init(p_full(s), 4);
+      mbar_init(o_full(s), 1);
+      mbar_init(flags_full(s), 2);
+      mbar_init(flags_free(s), 8);
+    }
+    mbar_init(final_bar, 1);
+    fence_mbar_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(sb + S_::OFF_TMEM, TMEM_COLS);
+    tmem_relinquish();
+  }
+  if (warp == TMA_WARP && lane == 0) {
+    prefetch_tmap(&tm_q);
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + S_::OFF_TMEM);
+  griddep_wait();
+  griddep_launch_dependents();
+
+  Items items;
+  Item it;
+  if (warp >= MMA_WARP) {
+    set_max_regs_down<OTHER_REGS>();
+    if (warp == TMA_WARP) {
+      // ------------------------------------------------------------ TMA --
+      uint32_t kv = 0, n = 0;   // ring uses, items
+      bool ok = true;
+      for (int64_t w = blockIdx.x; ok && items.get(p, w, it); w += gridDim.x, ++n) {
+        if (lane == 0) {
+          const int n0 = it.tiles(0, p.causal), n1 = it.tiles(1, p.causal);
+          const int tiles = max(n0, n1);
+          const int kh = it.head / p.group;
+          ok = svdq_wait(q_empty, (n & 1u) ^ 1u, SITE_TMA_Q);
+          if (ok) {
+            const int slots = n1 > 0 ? 2 : 1;
+            mbar_arrive_expect_tx(q_full, slots * S_::TILE_BYTES);
+            for (int s = 0; s < slots; ++s)
+              for (int b = 0; b < NB; ++b)
+                tma_load_3d(s_q(s) + b * BOX_BYTES, &tm_q, 64 * b, it.head,
+                            it.begin + it.q0 + s * ROWS, q_full);
+          }
+          for (int j = 0; ok && j < 2 * tiles; ++j, ++kv) {
+            const uint32_t st = kv % STAGES;
+            ok = svdq_wait(empty_bar(st), ((kv / STAGES) & 1u) ^ 1u, SITE_TMA_KV);
+            if (!ok) break;
+            mbar_arrive_expect_tx(full_bar(st), S_::TILE_BYTES);
+            for (int b = 0; b < NB; ++b)
+              tma_load_3d(s_kv(st) + b * BOX_BYTES, (j & 1) ? &tm_v : &tm_k, 64 * b, kh,
+                          it.begin + (j >> 1) * ROWS, full_bar(st));
+            if ((j & 1) && it.guarded(j >> 1, p.causal)) mbar_arrive(guard_go(st));
+          }
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      }
+      if (lane == 0) {
+        // Every copy issued has landed before the block exits (after an
+        // error nobody else may be waiting for them).
+        for (uint32_t j = 0; j < min(kv, static_cast<uint32_t>(STAGES)); ++j) {
+          const uint32_t u = kv - 1 - j;
+          drain_wait(full_bar(u % STAGES), (u / STAGES) & 1u, 50000000ull);
+        }
+        if (n > 0) drain_wait(q_full, (n - 1) & 1u, 50000000ull);
+      }
+      __syncwarp();
+    } else if (warp == MMA_WARP) {
+      // ------------------------------------------------------------ MMA --
+      const uint32_t dn = (p.D + 15) / 16 * 16;   // columns of O, and k of Q K^T
+      const int dk = dn / 16;
+      const uint32_t id_o = BF16 ? idesc_bf16_f32(ROWS, dn, 0, 1) : idesc_f16_f32(ROWS, dn, 0, 1);
+      uint32_t kv = 0, n = 0, phases = 0;   // ring uses, items, guarded uses by stage (parity)
+      uint32_t np[2] = {0, 0};    // P tiles waited for, by slot
+      bool ok = true;
+      for (int64_t w = blockIdx.x; ok && items.get(p, w, it); w += gridDim.x, ++n) {
+        if (lane == 0) {
+          const int nt[2] = {it.tiles(0, p.causal), it.tiles(1, p.causal)};
+          const int tiles = max(nt[0], nt[1]);
+          const int last = it.key_tiles() - 1;
+          const int last_steps = (it.len - last * ROWS + 15) / 16;   // 16-key steps of the last tile
+          auto qk = [&](int s, int j) {
+            const uint32_t keys = j == last ? 16 * last_steps : ROWS;
+            const uint32_t id = BF16 ? idesc_bf16_f32(ROWS, keys, 0, 0) : idesc_f16_f32(ROWS, keys, 0, 0);
+            const uint32_t kb = s_kv((kv + 2 * j) % STAGES);
+            for (int c = 0; c < dk; ++c) {
+              const uint32_t off = (c >> 2) * BOX_BYTES + 32 * (c & 3);
+              mma_f16(tmem + TM_S + ROWS * s, smem_desc(s_q(s) + off, 16, 1024, kLayoutSwizzle128B),
+                      smem_desc(kb + off, 16, 1024, kLayoutSwizzle128B), id, c != 0);
+            }
+            tc_commit(s_full(s));
+          };
+          auto wait_kv = [&](uint32_t u) {
+            const bool r = svdq_wait(full_bar(u % STAGES), (u / STAGES) & 1u, SITE_MMA_KV);
+            tc_fence_after();
+            return r;
+          };
+          ok = svdq_wait(q_full, n & 1u, SITE_MMA_Q) && wait_kv(kv);
+          if (ok) {
+            for (int s = 0; s < 2; ++s)
+              if (nt[s] > 0) qk(s, 0);
+            tc_commit(empty_bar(kv % STAGES));
+            if (tiles == 1) tc_commit(q_empty);
+          }
+          for (int j = 0; ok && j < tiles; ++j) {
+            const uint32_t uv = kv + 2 * j + 1, uk = uv + 1;
+            const uint32_t vb = s_kv(uv % STAGES);
+            const int steps = j == last ? last_steps : ROWS / 16;
+            const bool more = j + 1 < tiles;
+            ok = wait_kv(uv);
+            if (ok && it.guarded(j, p.causal)) {
+              const uint32_t st = uv % STAGES;
+              ok = svdq_wait(guard_done(st), (phases >> st) & 1u, SITE_MMA_GUARD);
+              phases ^= 1u << st;
+            }
+            if (ok && more) ok = wait_kv(uk);
+            for (int s = 0; ok && s < 2; ++s) {
+              if (j < nt[s]) {
+                ok = svdq_wait(p_full(s), np[s]++ & 1u, SITE_MMA_P);
+                if (!ok) break;
+                tc_fence_after();
+                for (int c = 0; c < steps; ++c)
+                  mma_f16_ts(tmem + TM_O + ROWS * s, tmem + TM_S + ROWS * s + 8 * c,
+                             smem_desc(vb + 2048 * c, BOX_BYTES, 1024, kLayoutSwizzle128B), id_o,
+                             (j | c) != 0);
+                if (j == nt[s] - 1) tc_commit(o_full(s));
+              }
+              if (j + 1 < nt[s]) qk(s, j + 1);
+            }
+            if (!ok) break;
+            tc_commit(empty_bar(uv % STAGES));
+            if (more) tc_commit(empty_bar(uk % STAGES));
+            if (j + 2 == tiles) tc_commit(q_empty);   // the last Q K^T is in flight
+          }
+          kv += 2 * tiles;
+        }
+        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+      }
+      if (lane == 0) {
+        // Every MMA this thread issued completes before TMEM is released.
+        tc_commit(final_bar);
+        drain_wait(final_bar, 0, 100000000ull);
+      }
+      __syncwarp();
+    } else {
+      // --------------------------------------------------------- guards --
+      const int g = warp - GUARD_WARP;
+      uint32_t kv = 0, n = 0, phases = 0;
+      bool ok = true;
+      for (int64_t w = blockIdx.x; ok && items.get(p, w, it); w += gridDim.x, ++n) {
+        const int tiles = max(it.tiles(0, p.causal), it.tiles(1, p.causal));
+        uint32_t* f = flags + 16 * (n & 1) + 8 * g;
+        if (p.causal) {
+          // the epilogues of the item before last have read these words
+          if (n >= 2)
+            ok = __all_sync(0xFFFFFFFFu, svdq_wait(flags_free(n & 1), ((n >> 1) & 1u) ^ 1u,
+                                                   SITE_GUARD_FLAGS));
+          if (!ok) break;
+          if (lane < 8) f[lane] = 0u;
+          __syncwarp();
+        }
+        for (int j = 0; ok && j < tiles; ++j) {
+          if (!it.guarded(j, p.causal)) continue;
+          const uint32_t u = kv + 2 * j + 1;
+          const uint32_t st = u % STAGES;
+          ok = __all_sync(0xFFFFFFFFu, svdq_wait(guard_go(st), (phases >> st) & 1u, SITE_GUARD_V) &&
+                                           svdq_wait(full_bar(st), (u / STAGES) & 1u, SITE_GUARD_V));
+          if (!ok) break;
+          phases ^= 1u << st;
+          const int valid = min(ROWS, it.len - j * ROWS);
+          const bool scan = p.causal && j >= it.q0 / ROWS;
+          uint32_t* fj = f + 4 * (j - it.q0 / ROWS);
+          const int stop = (valid + 15) / 16 * 16;
+          for (int c = 32 * g + lane; c < static_cast<int>(S_::TILE_BYTES / 16); c += 64) {
+            const int row = (c >> 3) & (ROWS - 1);
+            const uint32_t at = s_kv(st) + 16 * c;
+            if (row >= stop) continue;
+            if (row >= valid) {
+              st_shared_v4(at, 0u, 0u, 0u, 0u);
+            } else if (scan) {
+              uint32_t x[4];
+              ld_shared_v4(at, x[0], x[1], x[2], x[3]);
+              constexpr uint32_t m = BF16 ? 0x7F807F80u : 0x7C007C00u;
+              constexpr uint32_t one = BF16 ? 0x00800080u : 0x04000400u;
+              uint32_t bad = 0;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) bad |= ((x[i] & m) + one) & 0x80008000u;
+              if (bad != 0u) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  if (is_nonfinite16<BF16>(x[i])) x[i] &= 0xFFFF0000u;
+                  if (is_nonfinite16<BF16>(x[i] >> 16)) x[i] &= 0x0000FFFFu;
+                }
+                st_shared_v4(at, x[0], x[1], x[2], x[3]);
+                atomicOr(fj + (row >> 5), 1u << (row & 31));
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(guard_done(st));
+        }
+        if (ok && p.causal && lane == 0) mbar_arrive(flags_full(n & 1));
+        kv += 2 * tiles;
+      }
+    }
+  } else {
+    // ----------------------------------------------------------- softmax --
+    set_max_regs_up<SOFTMAX_REGS>();
+    const int slot = warp >> 2;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t tm_s = lane_base + TM_S + ROWS * slot;
+    const uint32_t tm_o = lane_base + TM_O + ROWS * slot;
+    const int r = (warp & 3) * 32 + lane;   // row of the slot
+    const float sc = p.scale_log2;
+    uint32_t ns = 0, no = 0, n = 0;         // S tiles, O tiles waited for, items
+    bool ok = true;
+    for (int64_t w = blockIdx.x; ok && items.get(p, w, it); w += gridDim.x, ++n) {
+      const int tiles = it.tiles(slot, p.causal);
+      const int row = it.q0 + slot * ROWS + r;   // of the sequence
+      if (tiles > 0) {
+        float m = -INFINITY;     // reference of the row, raw units of S
+        float l0 = 0.f, l1 = 0.f;
+        for (int j = 0; j < tiles; ++j) {
+          ok = __all_sync(0xFFFFFFFFu, svdq_wait(s_full(slot), ns++ & 1u, SITE_SOFT_S));
+          if (!ok) break;
+          tc_fence_after();
+          uint32_t x[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tm_s + 32 * c, x[c]);
+          tmem_ld_wait();
+          // keys at or behind `keys` are not this row's
+          const int keys = (p.causal ? min(it.len, row + 1) : it.len) - j * ROWS;
+          if (__any_sync(0xFFFFFFFFu, keys < ROWS)) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (32 * c + e >= keys) x[c][e] = 0xFF800000u;   // -inf
+          }
+          float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e) t[e & 3] = fmaxf(t[e & 3], __uint_as_float(x[c][e]));
+          const float top = fmaxf(m, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
+          if (j == 0) {
+            m = top;
+          } else if (__any_sync(0xFFFFFFFFu, (top - m) * sc > RESCALE_LOG2)) {
+            // O is idle here: the commit behind s_full also covers this
+            // slot's previous P V.
+            const float f = top == m ? 1.f : ex2_approx_ftz((m - top) * sc);
+            m = top;
+            l0 *= f;
+            l1 *= f;
+            for (int c = 0; c < p.D; c += 16) {
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(tm_o + c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+              tmem_st_32x32b_x16(tm_o + c, o);
+            }
+          }
+          // Exponents x sc - m sc in one fma: the rounding of m sc, 2^-24 of
+          // it, adds to the one S has anyway.  Where m sc is so large that
+          // this would show (2^-12 and more), m is taken off first.
+          float off = m == -INFINITY ? 0.f : -m * sc;
+          if (__any_sync(0xFFFFFFFFu, fabsf(off) > 4096.f)) {
+            const float ref = m == -INFINITY ? 0.f : m;
+            off = 0.f;
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+#pragma unroll
+              for (int e = 0; e < 32; ++e) x[c][e] = __float_as_uint(__uint_as_float(x[c][e]) - ref);
+          }
+          const uint64_t sc2 = pk(sc, sc), off2 = pk(off, off);
+          uint64_t sum2 = pk(l0, l1);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w16[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float a, b;
+              upk(fma2(pk(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sc2, off2), a, b);
+              a = ex2_approx_ftz(a);
+              b = ex2_approx_ftz(b);
+              sum2 = add2(sum2, pk(a, b));
+              w16[e] = pack2<BF16>(a, b);
+            }
+            tmem_st_32x32b_x16(tm_s + 16 * c, w16);
+          }
+          upk(sum2, l0, l1);
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full(slot));
+        }
+        if (!ok) break;
+        // -------------------------------------------------------- epilogue --
+        ok = __all_sync(0xFFFFFFFFu, svdq_wait(o_full(slot), no++ & 1u, SITE_SOFT_O));
+        if (!ok) break;
+        tc_fence_after();
+        const float inv = 1.f / (l0 + l1);
+        const uint32_t* f = flags + 16 * (n & 1);
+        uint32_t noted = 0;
+        if (p.causal) {
+          ok = __all_sync(0xFFFFFFFFu, svdq_wait(flags_full(n & 1), (n >> 1) & 1u, SITE_SOFT_FLAGS));
+          if (!ok) break;
+#pragma unroll
+          for (int i = 0; i < 16; ++i) noted |= f[i];
+        }
+        uint16_t* dst = p.out + static_cast<int64_t>(it.begin + row) * p.ost + it.head * p.osh;
+        for (int c = 0; c < p.D; c += 16) {
+          uint32_t o[16];
+          tmem_ld_32x32b_x16(tm_o + c, o);
+          tmem_ld_wait();
+          float v[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * inv;
+          if (noted != 0u) {
+            // Non-finite values of the diagonal tiles: into the rows that attend them.
+            for (int i = 0; i < 8; ++i) {
+              for (uint32_t b = f[i] | f[i + 8]; b != 0u; b &= b - 1) {
+                const int key = it.q0 + 32 * i + __ffs(b) - 1;
+                if (key > row) continue;
+                const uint16_t* src = p.v + static_cast<int64_t>(it.begin + key) * p.vst +
+                                      (it.head / p.group) * p.vsh + c;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                  if (c + e >= p.D) break;
+                  const uint32_t u = src[e];
+                  if (is_nonfinite16<BF16>(u))
+                    v[e] += BF16 ? __uint_as_float(u << 16)
+                                 : __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
+                }
+              }
+            }
+          }
+          if (row < it.len) {
+            const float (&a)[8] = reinterpret_cast<const float (&)[8]>(v[0]);
+            const float (&b)[8] = reinterpret_cast<const float (&)[8]>(v[8]);
+            *reinterpret_cast<uint4*>(dst + c) = pack8<BF16>(a);
+            if (c + 8 < p.D) *reinterpret_cast<uint4*>(dst + c + 8) = pack8<BF16>(b);
+          }
+        }
+        tc_fence_before();
+      }
+      if (p.causal) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(flags_free(n & 1));
+      }
+    }
+  }
+
+  // ----------------------------------------------------------- teardown --
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == MMA_WARP) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+}  // namespace ka
+}  // namespace svdq

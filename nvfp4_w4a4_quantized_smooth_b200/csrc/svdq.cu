@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <cudaTypedefs.h>
 
+#include <climits>
+#include <cmath>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -17,6 +19,9 @@
 #include "ks_w4a4_linear_small.cuh"
 #include "kr_scales.cuh"
 #include "kw_quantize_weights.cuh"
+#include "kn_norm_gate.cuh"
+#include "kp_rope_qk.cuh"
+#include "ka_attention.cuh"
 
 namespace {
 
@@ -33,6 +38,9 @@ struct DeviceInfo {
   int ks_clusters[9];
   // Max co-resident CTA pairs of the pair GEMM; -1 = not queried yet.
   int kg2_pairs = -1;
+  // The attention kernels have been given their shared memory and have the
+  // registers their warp roles share out.
+  bool ka_ready = false;
 };
 
 std::mutex g_mu;
@@ -1001,6 +1009,351 @@ int svdq_set_wait_timeout_ns(uint64_t ns) {
   if (cudaMemcpyToSymbol(svdq::g_wait_limit_ns, &v, sizeof(v)) != cudaSuccess)
     return SVDQ_ERR_CUDA;
   return SVDQ_OK;
+}
+
+}  // extern "C"
+
+// ---- between the linears of a block ---------------------------------------
+
+namespace {
+
+// A strided operand as bytes: `outer` rows `st` apart of `inner` pieces `sh`
+// apart, each `bytes` long (strides positive, in bytes).
+struct Extent {
+  uintptr_t base;
+  int64_t outer, st, inner, sh, bytes;
+  int64_t span() const { return (outer - 1) * st + (inner - 1) * sh + bytes; }
+};
+
+Extent extent(const void* p, int64_t outer, int64_t st, int64_t inner, int64_t sh, int64_t cols) {
+  return {reinterpret_cast<uintptr_t>(p), outer, 2 * st, inner, 2 * sh, 2 * cols};
+}
+
+bool same(const Extent& a, const Extent& b) {
+  return a.base == b.base && (a.st == b.st || a.outer == 1) && (a.sh == b.sh || a.inner == 1);
+}
+
+// Whether two operands may share a byte.  Exact for ranges that do not meet
+// and for operands side by side in the rows of one buffer (same outer
+// stride, pieces within it); otherwise it says yes.
+bool may_meet(const Extent& a, const Extent& b) {
+  const int64_t d = static_cast<int64_t>(b.base - a.base);
+  if (d >= a.span() || -d >= b.span()) return false;
+  const int64_t ea = (a.inner - 1) * a.sh + a.bytes, eb = (b.inner - 1) * b.sh + b.bytes;
+  if (a.st == b.st && a.outer > 1 && b.outer > 1 && ea <= a.st && eb <= b.st) {
+    const int64_t off = ((d % a.st) + a.st) % a.st;   // b's row begins this far into a's
+    return !(off >= ea && off + eb <= a.st);
+  }
+  return true;
+}
+
+// An output may be exactly an input (each element is read before it is
+// written, by the same thread), or else has to lie apart from it.
+bool bad_overlap(const Extent& out, const Extent& in) { return !same(out, in) && may_meet(out, in); }
+
+// Launch configuration with programmatic stream serialization, as the other
+// kernels of the layer.
+void pdl_config(cudaLaunchConfig_t* cfg, cudaLaunchAttribute* attr, unsigned grid, unsigned block,
+                size_t smem, void* stream) {
+  std::memset(cfg, 0, sizeof(*cfg));
+  cfg->gridDim = dim3(grid, 1, 1);
+  cfg->blockDim = dim3(block, 1, 1);
+  cfg->dynamicSmemBytes = smem;
+  cfg->stream = static_cast<cudaStream_t>(stream);
+  attr->id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr->val.programmaticStreamSerializationAllowed = 1;
+  cfg->attrs = attr;
+  cfg->numAttrs = 1;
+}
+
+template <bool BF16>
+cudaError_t launch_kn(cudaLaunchConfig_t& cfg, int vpt, const svdq::kn::Params& p) {
+  using namespace svdq::kn;
+  return vpt == 1 ? cudaLaunchKernelEx(&cfg, norm_gate_kernel<BF16, 1>, p)
+                  : cudaLaunchKernelEx(&cfg, norm_gate_kernel<BF16, 2>, p);
+}
+
+template <bool BF16, int NB>
+int prepare_ka() {
+  using namespace svdq::ka;
+  const auto fn = attention_kernel<BF16, NB>;
+  cudaFuncAttributes a;
+  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           svdq::ka::Shape<NB>::SMEM_BYTES) != cudaSuccess ||
+      cudaFuncGetAttributes(&a, fn) != cudaSuccess)
+    return SVDQ_ERR_CUDA;
+  // The warp roles' register shares come out of the block's registers.
+  return a.numRegs * NUM_THREADS >= SOFTMAX_REGS * 256 + OTHER_REGS * 128 ? SVDQ_OK
+                                                                          : SVDQ_ERR_UNSUPPORTED;
+}
+
+int ka_setup(DeviceInfo* d) {
+  std::lock_guard<std::mutex> lock(g_mu);
+  if (d->ka_ready) return SVDQ_OK;
+  int st = prepare_ka<true, 1>();
+  if (!st) st = prepare_ka<true, 2>();
+  if (!st) st = prepare_ka<false, 1>();
+  if (!st) st = prepare_ka<false, 2>();
+  if (st) return st;
+  d->ka_ready = true;
+  return SVDQ_OK;
+}
+
+bool bad_norm(int kind) { return kind < 0 || kind > SVDQ_NORM_LAYER; }
+
+}  // namespace
+
+extern "C" {
+
+int svdq_norm_gate_residual(int dtype, const uint16_t* x, int64_t ldx, const uint16_t* y,
+                            int64_t ldy, int T, int C, const int32_t* cu_seqlens, int n_seqs,
+                            int post, const uint16_t* post_weight, int gate_kind,
+                            const uint16_t* gate, int64_t ld_gate, float residual_scale, int pre,
+                            const uint16_t* pre_weight, const uint16_t* scale, int64_t ld_scale,
+                            const uint16_t* shift, int64_t ld_shift, float eps, uint16_t* h,
+                            int64_t ldh, uint16_t* n, int64_t ldn, void* stream) {
+  if (dtype != SVDQ_BF16 && dtype != SVDQ_FP16) return SVDQ_ERR_INVALID_ARG;
+  if (bad_norm(post) || bad_norm(pre) || gate_kind < 0 || gate_kind > SVDQ_GATE_TANH)
+    return SVDQ_ERR_INVALID_ARG;
+  if (T < 0 || C < 1 || n_seqs < 1 || (!cu_seqlens && n_seqs != 1)) return SVDQ_ERR_SHAPE;
+  if (!std::isfinite(eps) || eps < 0.f || !std::isfinite(residual_scale))
+    return SVDQ_ERR_INVALID_ARG;
+  if ((gate_kind != SVDQ_GATE_NONE) != (gate != nullptr)) return SVDQ_ERR_INVALID_ARG;
+  if ((post == SVDQ_NORM_NONE && post_weight) || (pre == SVDQ_NORM_NONE && pre_weight))
+    return SVDQ_ERR_INVALID_ARG;
+  if (C % 8 || C > svdq::kn::MAX_C) return SVDQ_ERR_UNSUPPORTED;
+  if (T == 0) return SVDQ_OK;
+  if (!x || (y && !h) || (!y && !n)) return SVDQ_ERR_INVALID_ARG;
+  if (!y && (h || post != SVDQ_NORM_NONE || gate || residual_scale != 1.f))
+    return SVDQ_ERR_INVALID_ARG;
+  if (!n && (pre != SVDQ_NORM_NONE || scale || shift)) return SVDQ_ERR_INVALID_ARG;
+  if (ldx < C || (y && (ldy < C || ldh < C)) || (n && ldn < C) || (gate && ld_gate < 0) ||
+      (scale && ld_scale < 0) || (shift && ld_shift < 0))
+    return SVDQ_ERR_SHAPE;
+  if (!aligned(x, 16) || ldx % 8 || (y && (!aligned(y, 16) || ldy % 8 || !aligned(h, 16) || ldh % 8)) ||
+      (n && (!aligned(n, 16) || ldn % 8)) || (gate && (!aligned(gate, 16) || ld_gate % 8)) ||
+      (scale && (!aligned(scale, 16) || ld_scale % 8)) ||
+      (shift && (!aligned(shift, 16) || ld_shift % 8)) || !aligned(post_weight, 16) ||
+      !aligned(pre_weight, 16) || !aligned(cu_seqlens, 4))
+    return SVDQ_ERR_ALIGNMENT;
+  const Extent ex = extent(x, T, ldx, 1, C, C);
+  const Extent ey = extent(y, T, ldy, 1, C, C);
+  const Extent eh = extent(h, T, ldh, 1, C, C);
+  const Extent en = extent(n, T, ldn, 1, C, C);
+  if ((y && (bad_overlap(eh, ex) || bad_overlap(eh, ey))) ||
+      (n && (bad_overlap(en, ex) || (y && (bad_overlap(en, ey) || may_meet(en, eh))))))
+    return SVDQ_ERR_INVALID_ARG;
+  const Extent vec[] = {extent(gate, n_seqs, ld_gate, 1, C, C), extent(scale, n_seqs, ld_scale, 1, C, C),
+                        extent(shift, n_seqs, ld_shift, 1, C, C), extent(post_weight, 1, C, 1, C, C),
+                        extent(pre_weight, 1, C, 1, C, C)};
+  for (const Extent& v : vec)
+    if (v.base && ((y && may_meet(eh, v)) || (n && may_meet(en, v)))) return SVDQ_ERR_INVALID_ARG;
+  DeviceInfo* d = nullptr;
+  if (int st = device_setup(&d)) return st;
+
+  svdq::kn::Params p;
+  p.x = x, p.y = y, p.gate = gate, p.scale = scale, p.shift = shift;
+  p.post_w = post_weight, p.pre_w = pre_weight, p.h = h, p.n = n, p.cu = cu_seqlens;
+  p.ldx = ldx, p.ldy = ldy, p.ldh = ldh, p.ldn = ldn;
+  p.ldg = ld_gate, p.lds = ld_scale, p.ldb = ld_shift;
+  p.T = T, p.C = C, p.S = n_seqs, p.post = post, p.pre = pre, p.gate_kind = gate_kind;
+  p.a = residual_scale, p.eps = eps, p.inv_c = 1.f / static_cast<float>(C);
+  // 8-element words per thread: as many threads as words up to 512.
+  const int words = C / 8;
+  const int vpt = words <= svdq::kn::MAX_THREADS ? 1 : 2;
+  const int threads = ((words + vpt - 1) / vpt + 31) / 32 * 32;
+  // As many blocks as run at once (by threads), each with its run of rows.
+  const int blocks = d->num_sms * (1024 / threads > 8 ? 8 : 1024 / threads);
+  p.rows_per_block = (T + blocks - 1) / blocks;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  pdl_config(&cfg, &attr, (T + p.rows_per_block - 1) / p.rows_per_block, threads, 0, stream);
+  const cudaError_t e = dtype == SVDQ_BF16 ? launch_kn<true>(cfg, vpt, p) : launch_kn<false>(cfg, vpt, p);
+  if (e != cudaSuccess) return SVDQ_ERR_CUDA;
+  return launch_status();
+}
+
+int svdq_rope_turns(const int* axes, int n_axes, double theta, double* turns) {
+  if (!axes || !turns || n_axes < 1 || n_axes > svdq::kp::MAX_AXES || !std::isfinite(theta) ||
+      theta <= 0.0)
+    return SVDQ_ERR_INVALID_ARG;
+  int R = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (axes[a] < 2 || axes[a] % 2 || axes[a] > svdq::kp::MAX_D) return SVDQ_ERR_SHAPE;
+    R += axes[a];
+  }
+  if (R > svdq::kp::MAX_D) return SVDQ_ERR_UNSUPPORTED;
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  for (int a = 0; a < n_axes; ++a)
+    for (int i = 0; i < axes[a] / 2; ++i)
+      *turns++ = std::pow(theta, -2.0 * i / axes[a]) / kTwoPi;
+  return SVDQ_OK;
+}
+
+int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, int Hq,
+                 const uint16_t* k, int64_t k_stride_t, int64_t k_stride_h, int Hk, int T, int D,
+                 const int32_t* positions, int64_t ld_pos, const int* axes, int n_axes,
+                 const double* turns, int interleaved, const uint16_t* q_weight,
+                 const uint16_t* k_weight, float eps, uint16_t* q_out, int64_t qo_stride_t,
+                 int64_t qo_stride_h, uint16_t* k_out, int64_t ko_stride_t, int64_t ko_stride_h,
+                 void* stream) {
+  if (dtype != SVDQ_BF16 && dtype != SVDQ_FP16) return SVDQ_ERR_INVALID_ARG;
+  if (!axes || !turns || n_axes < 1 || n_axes > svdq::kp::MAX_AXES || !std::isfinite(eps) || eps < 0.f)
+    return SVDQ_ERR_INVALID_ARG;
+  if (T < 0 || Hq < 0 || Hk < 0 || Hq + static_cast<int64_t>(Hk) < 1 || D < 1) return SVDQ_ERR_SHAPE;
+  int R = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    if (axes[a] < 2 || axes[a] % 2 || axes[a] > D) return SVDQ_ERR_SHAPE;
+    R += axes[a];
+  }
+  if (R > D) return SVDQ_ERR_SHAPE;
+  if (D % 8 || D > svdq::kp::MAX_D || (!interleaved && R % 16) ||
+      Hq + static_cast<int64_t>(Hk) > (1 << 16))
+    return SVDQ_ERR_UNSUPPORTED;
+  if (T == 0) return SVDQ_OK;
+  const bool has_q = Hq > 0, has_k = Hk > 0;
+  if (!positions || (has_q && (!q || !q_out)) || (has_k && (!k || !k_out)) ||
+      (!has_q && (q || q_out || q_weight)) || (!has_k && (k || k_out || k_weight)))
+    return SVDQ_ERR_INVALID_ARG;
+  if (ld_pos < n_axes) return SVDQ_ERR_SHAPE;
+  auto bad_strides = [&](int64_t st, int64_t sh, int H) {
+    return (T > 1 && st < D) || (H > 1 && sh < D);
+  };
+  if ((has_q && (bad_strides(q_stride_t, q_stride_h, Hq) || bad_strides(qo_stride_t, qo_stride_h, Hq))) ||
+      (has_k && (bad_strides(k_stride_t, k_stride_h, Hk) || bad_strides(ko_stride_t, ko_stride_h, Hk))))
+    return SVDQ_ERR_SHAPE;
+  auto misaligned = [&](const void* ptr, int64_t st, int64_t sh, int H) {
+    return !aligned(ptr, 16) || (T > 1 && st % 8) || (H > 1 && sh % 8);
+  };
+  if ((has_q && (misaligned(q, q_stride_t, q_stride_h, Hq) ||
+                 misaligned(q_out, qo_stride_t, qo_stride_h, Hq))) ||
+      (has_k && (misaligned(k, k_stride_t, k_stride_h, Hk) ||
+                 misaligned(k_out, ko_stride_t, ko_stride_h, Hk))) ||
+      !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(positions, 4))
+    return SVDQ_ERR_ALIGNMENT;
+  if (T == 1) q_stride_t = k_stride_t = qo_stride_t = ko_stride_t = D;   // not used
+  if (Hq <= 1) q_stride_h = qo_stride_h = D;
+  if (Hk <= 1) k_stride_h = ko_stride_h = D;
+  const Extent eq = extent(q, T, q_stride_t, Hq, q_stride_h, D);
+  const Extent ek = extent(k, T, k_stride_t, Hk, k_stride_h, D);
+  const Extent eqo = extent(q_out, T, qo_stride_t, Hq, qo_stride_h, D);
+  const Extent eko = extent(k_out, T, ko_stride_t, Hk, ko_stride_h, D);
+  const Extent epos = {reinterpret_cast<uintptr_t>(positions), T, 4 * ld_pos, 1, 4, 4 * n_axes};
+  if ((has_q && (bad_overlap(eqo, eq) || may_meet(eqo, epos))) ||
+      (has_k && (bad_overlap(eko, ek) || may_meet(eko, epos))) ||
+      (has_q && has_k && (may_meet(eqo, ek) || may_meet(eko, eq) || may_meet(eqo, eko))))
+    return SVDQ_ERR_INVALID_ARG;
+  const Extent ws[] = {extent(q_weight, 1, D, 1, D, D), extent(k_weight, 1, D, 1, D, D)};
+  for (const Extent& w : ws)
+    if (w.base && ((has_q && may_meet(eqo, w)) || (has_k && may_meet(eko, w))))
+      return SVDQ_ERR_INVALID_ARG;
+  DeviceInfo* d = nullptr;
+  if (int st = device_setup(&d)) return st;
+
+  svdq::kp::Params p;
+  std::memset(&p, 0, sizeof(p));
+  p.q = q, p.k = k, p.qw = q_weight, p.kw = k_weight, p.qo = q_out, p.ko = k_out, p.pos = positions;
+  p.qst = q_stride_t, p.qsh = q_stride_h, p.kst = k_stride_t, p.ksh = k_stride_h;
+  p.qost = qo_stride_t, p.qosh = qo_stride_h, p.kost = ko_stride_t, p.kosh = ko_stride_h;
+  p.ldpos = ld_pos;
+  p.T = T, p.Hq = Hq, p.Hk = Hk, p.D = D, p.half = R / 2, p.axes = n_axes;
+  p.lanes = 1;
+  while (p.lanes < D / 8) p.lanes *= 2;
+  p.pairs = interleaved ? 1 : 0;
+  p.eps = eps, p.inv_d = 1.f / static_cast<float>(D);
+  int at = 0;
+  for (int a = 0; a < n_axes; ++a) {
+    p.first[a] = at;
+    at += axes[a] / 2;
+  }
+  p.first[n_axes] = at;
+  std::memcpy(p.turns, turns, sizeof(double) * at);
+  // Tokens per block: enough that every thread has an angle to compute and
+  // several words in flight, while the blocks still fill the device.
+  p.tokens = svdq::kp::MAX_TOKENS;
+  while (p.tokens > 1 && (T + p.tokens - 1) / p.tokens < 4 * d->num_sms) p.tokens /= 2;
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  pdl_config(&cfg, &attr, (T + p.tokens - 1) / p.tokens, svdq::kp::THREADS, 0, stream);
+  const cudaError_t e = dtype == SVDQ_BF16
+                            ? cudaLaunchKernelEx(&cfg, svdq::kp::rope_qk_kernel<true>, p)
+                            : cudaLaunchKernelEx(&cfg, svdq::kp::rope_qk_kernel<false>, p);
+  if (e != cudaSuccess) return SVDQ_ERR_CUDA;
+  return launch_status();
+}
+
+int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h,
+                   const uint16_t* k, int64_t k_stride_t, int64_t k_stride_h, const uint16_t* v,
+                   int64_t v_stride_t, int64_t v_stride_h, int T, int Hq, int Hk, int D,
+                   const int32_t* cu_seqlens, int n_seqs, int causal, float scale, uint16_t* out,
+                   int64_t o_stride_t, int64_t o_stride_h, void* stream) {
+  if (dtype != SVDQ_BF16 && dtype != SVDQ_FP16) return SVDQ_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || scale <= 0.f) return SVDQ_ERR_INVALID_ARG;
+  if (T < 0 || Hq < 1 || Hk < 1 || Hq % Hk || D < 1 || n_seqs < 1 || (!cu_seqlens && n_seqs != 1))
+    return SVDQ_ERR_SHAPE;
+  if (D % 8 || D > svdq::ka::MAX_D ||
+      (static_cast<int64_t>(T) / svdq::ka::ITEM_ROWS + 1) * Hq > INT_MAX)
+    return SVDQ_ERR_UNSUPPORTED;
+  if (T == 0) return SVDQ_OK;
+  if (!q || !k || !v || !out) return SVDQ_ERR_INVALID_ARG;
+  auto bad_strides = [&](int64_t st, int64_t sh, int H) {
+    return (T > 1 && st < D) || (H > 1 && sh < D);
+  };
+  if (bad_strides(q_stride_t, q_stride_h, Hq) || bad_strides(k_stride_t, k_stride_h, Hk) ||
+      bad_strides(v_stride_t, v_stride_h, Hk) || bad_strides(o_stride_t, o_stride_h, Hq))
+    return SVDQ_ERR_SHAPE;
+  auto misaligned = [&](const void* ptr, int64_t st, int64_t sh, int H) {
+    return !aligned(ptr, 16) || (T > 1 && st % 8) || (H > 1 && sh % 8);
+  };
+  if (misaligned(q, q_stride_t, q_stride_h, Hq) || misaligned(k, k_stride_t, k_stride_h, Hk) ||
+      misaligned(v, v_stride_t, v_stride_h, Hk) || misaligned(out, o_stride_t, o_stride_h, Hq) ||
+      !aligned(cu_seqlens, 4))
+    return SVDQ_ERR_ALIGNMENT;
+  // Strides of a dimension of one are not used.
+  if (T == 1) q_stride_t = k_stride_t = v_stride_t = o_stride_t = D;
+  if (Hq == 1) q_stride_h = o_stride_h = D;
+  if (Hk == 1) k_stride_h = v_stride_h = D;
+  const int64_t limit = int64_t{1} << 38;   // elements; a tensor map's strides end at 2^40 bytes
+  for (int64_t s : {q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h})
+    if (s > limit) return SVDQ_ERR_UNSUPPORTED;
+  const Extent eq = extent(q, T, q_stride_t, Hq, q_stride_h, D);
+  const Extent ek = extent(k, T, k_stride_t, Hk, k_stride_h, D);
+  const Extent ev = extent(v, T, v_stride_t, Hk, v_stride_h, D);
+  const Extent eo = extent(out, T, o_stride_t, Hq, o_stride_h, D);
+  if (may_meet(eo, eq) || may_meet(eo, ek) || may_meet(eo, ev)) return SVDQ_ERR_INVALID_ARG;
+  DeviceInfo* d = nullptr;
+  if (int st = device_setup(&d)) return st;
+  if (int st = ka_setup(d)) return st;
+
+  namespace ka = svdq::ka;
+  const CUtensorMapDataType dt =
+      dtype == SVDQ_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+  CUtensorMap tm_q, tm_k, tm_v;
+  if (make_tmap3(&tm_q, q, dt, D, Hq, T, 2 * q_stride_h, 2 * q_stride_t, 64, 1, ka::ROWS) ||
+      make_tmap3(&tm_k, k, dt, D, Hk, T, 2 * k_stride_h, 2 * k_stride_t, 64, 1, ka::ROWS) ||
+      make_tmap3(&tm_v, v, dt, D, Hk, T, 2 * v_stride_h, 2 * v_stride_t, 64, 1, ka::ROWS))
+    return SVDQ_ERR_CUDA;
+  ka::Params p;
+  p.cu = cu_seqlens, p.v = v, p.out = out;
+  p.vst = v_stride_t, p.vsh = v_stride_h, p.ost = o_stride_t, p.osh = o_stride_h;
+  p.T = T, p.S = n_seqs, p.Hq = Hq, p.group = Hq / Hk, p.D = D, p.causal = causal ? 1 : 0;
+  p.scale_log2 = scale * 1.44269504088896341f;
+  // At most this many work items; one persistent block per SM takes them in turn.
+  const int64_t items = (static_cast<int64_t>(T) / ka::ITEM_ROWS + n_seqs) * Hq;
+  const unsigned grid = static_cast<unsigned>(items < d->num_sms ? items : d->num_sms);
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  const bool wide = D > 64;
+  pdl_config(&cfg, &attr, grid, ka::NUM_THREADS,
+             wide ? ka::Shape<2>::SMEM_BYTES : ka::Shape<1>::SMEM_BYTES, stream);
+  const cudaError_t e =
+      dtype == SVDQ_BF16
+          ? (wide ? cudaLaunchKernelEx(&cfg, ka::attention_kernel<true, 2>, tm_q, tm_k, tm_v, p)
+                  : cudaLaunchKernelEx(&cfg, ka::attention_kernel<true, 1>, tm_q, tm_k, tm_v, p))
+          : (wide ? cudaLaunchKernelEx(&cfg, ka::attention_kernel<false, 2>, tm_q, tm_k, tm_v, p)
+                  : cudaLaunchKernelEx(&cfg, ka::attention_kernel<false, 1>, tm_q, tm_k, tm_v, p));
+  if (e != cudaSuccess) return SVDQ_ERR_CUDA;
+  return launch_status();
 }
 
 }  // extern "C"

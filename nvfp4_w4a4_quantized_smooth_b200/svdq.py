@@ -35,11 +35,22 @@ SCALES_WEIGHT = 1
 GEMM_TOKEN_MAJOR = 0
 GEMM_FEW_TOKENS = 1
 GEMM_PAIRS = 2
+BF16 = 0
+FP16 = 1
+NORM_NONE = 0
+NORM_RMS = 1
+NORM_LAYER = 2
+GATE_NONE = 0
+GATE_LINEAR = 1
+GATE_TANH = 2
 
 # Every symbol include/svdq.h declares, with (restype, argtypes).
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
+_L = ctypes.c_int64
+_F = ctypes.c_float
+_D = ctypes.c_double
 SIGNATURES = {
     "svdq_status_string": (ctypes.c_char_p, [_I]),
     "svdq_abi_version": (_I, []),
@@ -60,6 +71,13 @@ SIGNATURES = {
     "svdq_weight_workspace_bytes": (_SZ, [_I]),
     "svdq_quantize_weights": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _P]),
     "svdq_quantize_weights_noalloc": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _P]),
+    "svdq_norm_gate_residual": (_I, [_I, _P, _L, _P, _L, _I, _I, _P, _I, _I, _P, _I, _P, _L, _F,
+                                     _I, _P, _P, _L, _P, _L, _F, _P, _L, _P, _L, _P]),
+    "svdq_rope_turns": (_I, [_P, _I, _D, _P]),
+    "svdq_rope_qk": (_I, [_I, _P, _L, _L, _I, _P, _L, _L, _I, _I, _I, _P, _L, _P, _I, _P, _I, _P,
+                          _P, _F, _P, _L, _L, _P, _L, _L, _P]),
+    "svdq_attention": (_I, [_I, _P, _L, _L, _P, _L, _L, _P, _L, _L, _I, _I, _I, _I, _P, _I, _I,
+                            _F, _P, _L, _L, _P]),
     "svdq_check_device_error": (_I, [_P]),
     "svdq_set_wait_timeout_ns": (_I, [ctypes.c_uint64]),
     "svdq_wait_probe": (_I, [_I, _P]),
@@ -378,6 +396,245 @@ def quantize_weights(W: torch.Tensor, smooth: torch.Tensor, R: int = 128, stream
                proj_down=proj_down, proj_up=proj_up)
     if return_lowrank:
         out["lowrank"] = lowrank
+    return out
+
+
+# ---- between the linears of a block -----------------------------------------
+
+_DTYPES = {torch.bfloat16: BF16, torch.float16: FP16}
+_NORMS = {None: NORM_NONE, "rms": NORM_RMS, "layer": NORM_LAYER}
+
+
+class _On:
+    """The device of a call's tensors made current, and its stream: the given
+    one, or the device's current one.  Outputs allocated inside belong to
+    that stream."""
+
+    __slots__ = ("dev", "stream", "ctx")
+
+    def __init__(self, dev: torch.device, stream: Optional[torch.cuda.Stream]):
+        self.dev = dev
+        self.stream = stream
+        self.ctx = None
+        if stream is not None:
+            if stream.device != dev:
+                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+            self.ctx = torch.cuda.stream(stream)       # also makes its device current
+        elif dev.index != torch.cuda.current_device():
+            self.ctx = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.dev)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _need_like(t: Optional[torch.Tensor], first: torch.Tensor, shape, name: str) -> int:
+    """Check an optional operand against the call's first tensor; its address
+    (None for None)."""
+    if t is None:
+        return None
+    if t.dtype is not first.dtype or t.device != first.device:
+        raise ValueError(f"{name} must be {first.dtype} on {first.device}, "
+                         f"got {t.dtype} on {t.device}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must have unit stride along its last dimension")
+    return t.data_ptr()
+
+
+def _need_16bit(t: torch.Tensor, name: str, dim: int) -> int:
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dims")
+    return code
+
+
+def _need_cu(cu: Optional[torch.Tensor], dev: torch.device):
+    """(address, number of sequences) of cu_seqlens."""
+    if cu is None:
+        return None, 1
+    if cu.dtype is not torch.int32 or cu.device != dev or cu.dim() != 1 or cu.shape[0] < 2:
+        raise ValueError(f"cu_seqlens must be an int32 vector of at least 2 on {dev}")
+    if not cu.is_contiguous():
+        raise ValueError("cu_seqlens must be contiguous")
+    return cu.data_ptr(), cu.shape[0] - 1
+
+
+def norm_gate_residual(x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
+                       gate: Optional[torch.Tensor] = None, scale: Optional[torch.Tensor] = None,
+                       shift: Optional[torch.Tensor] = None,
+                       post_weight: Optional[torch.Tensor] = None,
+                       pre_weight: Optional[torch.Tensor] = None, post: Optional[str] = None,
+                       pre: Optional[str] = "rms", eps: float = 1e-6, gate_tanh: bool = False,
+                       residual_scale: float = 1.0, cu_seqlens: Optional[torch.Tensor] = None,
+                       h: Optional[torch.Tensor] = None, n: Optional[torch.Tensor] = None,
+                       stream=None):
+    """The norms before and after a block with its gate and residual scale:
+
+        h = residual_scale * x + gate * post(y)
+        n = pre(h) * (1 + scale) + shift
+
+    x, y [T, C] bf16 or fp16; gate, scale, shift [n_seqs, C] (tanh(gate) with
+    gate_tanh), rows by cu_seqlens [n_seqs + 1] int32; post, pre: None, "rms"
+    or "layer" with their weights [C] -> (h, n).  y None (the first norm of a
+    stack): h is x itself.  pre None without scale and shift: n is None.
+    h and n may be given, also exactly x or y; rows in no sequence are left
+    as they are."""
+    code = _need_16bit(x, "x", 2)
+    if post not in _NORMS or pre not in _NORMS:
+        raise ValueError('post and pre must be None, "rms" or "layer"')
+    T, C = x.shape
+    dev = x.device
+    px = _need_like(x, x, (T, C), "x")
+    py = _need_like(y, x, (T, C), "y")
+    cu, S = _need_cu(cu_seqlens, dev)
+    pg = _need_like(gate, x, (S, C), "gate")
+    ps = _need_like(scale, x, (S, C), "scale")
+    pb = _need_like(shift, x, (S, C), "shift")
+    pw = _need_like(post_weight, x, (C,), "post_weight")
+    qw = _need_like(pre_weight, x, (C,), "pre_weight")
+    if y is None and h is not None:
+        raise ValueError("h needs y (without y it is x itself)")
+    want_n = pre is not None or scale is not None or shift is not None
+    if n is not None and not want_n and y is None:
+        raise ValueError("nothing to compute: neither y nor pre, scale or shift")
+    with _On(dev, stream) as s:
+        if y is not None and h is None:
+            h = torch.empty(T, C, dtype=x.dtype, device=dev)
+        if want_n and n is None:
+            n = torch.empty(T, C, dtype=x.dtype, device=dev)
+        ph = _need_like(h, x, (T, C), "h")
+        pn = _need_like(n, x, (T, C), "n")
+
+        def ld(t, rows):
+            return 0 if t is None else t.stride(0) if rows > 1 else C
+
+        _check(_lib.svdq_norm_gate_residual(
+            code, px, ld(x, T), py, ld(y, T), T, C, cu, S, _NORMS[post], pw,
+            GATE_NONE if gate is None else GATE_TANH if gate_tanh else GATE_LINEAR, pg,
+            ld(gate, S), residual_scale, _NORMS[pre], qw, ps, ld(scale, S), pb, ld(shift, S), eps,
+            ph, ld(h, T), pn, ld(n, T), s),
+            "svdq_norm_gate_residual")
+    return (x if y is None else h), n
+
+
+class RopePlan:
+    """Frequencies of rope_qk, computed once: axes are the even widths of the
+    rotated dimensions of each position axis, sum(axes) <= head_dim; pairs are
+    (2p, 2p + 1), or (p, p + sum(axes) / 2) with interleaved False."""
+
+    def __init__(self, axes, theta: float, head_dim: int, interleaved: bool = True):
+        self.axes = tuple(int(a) for a in axes)
+        self.theta = float(theta)
+        self.head_dim = int(head_dim)
+        self.interleaved = bool(interleaved)
+        if sum(self.axes) > self.head_dim:
+            raise ValueError(f"axes {self.axes} exceed the head's {self.head_dim}")
+        self._axes = (ctypes.c_int * max(1, len(self.axes)))(*self.axes)
+        self._turns = (ctypes.c_double * max(1, sum(max(0, a) for a in self.axes) // 2))()
+        _check(_lib.svdq_rope_turns(self._axes, len(self.axes), self.theta, self._turns),
+               "svdq_rope_turns")
+
+
+def _head_strides(t: torch.Tensor):
+    return t.stride(0), t.stride(1)
+
+
+def rope_qk(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.Tensor,
+            plan: RopePlan, q_weight: Optional[torch.Tensor] = None,
+            k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6,
+            q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+            stream=None):
+    """Rotary positions with several axes on q [T, Hq, D] and k [T, Hk, D]
+    (bf16 or fp16, strided views allowed, either may be None), after their
+    per-head RMS norm where a weight [D] is given -> (q_out, k_out).
+
+    positions [T, len(plan.axes)] int32.  In place: q_out=q, k_out=k."""
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("rope_qk needs q or k")
+    code = _need_16bit(first, "q" if q is not None else "k", 3)
+    T, _, D = first.shape
+    dev = first.device
+    if D != plan.head_dim:
+        raise ValueError(f"heads of {D}, the plan is for {plan.head_dim}")
+    if k is not None and k.dim() != 3:
+        raise ValueError("k must have 3 dims")
+    Hq = 0 if q is None else q.shape[1]
+    Hk = 0 if k is None else k.shape[1]
+    A = len(plan.axes)
+    if (positions.dtype is not torch.int32 or positions.device != dev
+            or tuple(positions.shape) != (T, A)):
+        raise ValueError(f"positions must be int32 [{T}, {A}] on {dev}")
+    if positions.stride(1) != 1 and A > 1:
+        raise ValueError("positions must have unit stride along the axes")
+    if (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError("an output without its input")
+    pq = _need_like(q, first, (T, Hq, D), "q")
+    pk = _need_like(k, first, (T, Hk, D), "k")
+    wq = _need_like(q_weight, first, (D,), "q_weight")
+    wk = _need_like(k_weight, first, (D,), "k_weight")
+    with _On(dev, stream) as s:
+        if q is not None and q_out is None:
+            q_out = torch.empty(T, Hq, D, dtype=q.dtype, device=dev)
+        if k is not None and k_out is None:
+            k_out = torch.empty(T, Hk, D, dtype=k.dtype, device=dev)
+        pqo = _need_like(q_out, first, (T, Hq, D), "q_out")
+        pko = _need_like(k_out, first, (T, Hk, D), "k_out")
+        none = (0, 0)
+        _check(_lib.svdq_rope_qk(
+            code, pq, *(none if q is None else _head_strides(q)), Hq,
+            pk, *(none if k is None else _head_strides(k)), Hk, T, D,
+            positions.data_ptr(), positions.stride(0) if T > 1 else A, plan._axes, A, plan._turns,
+            1 if plan.interleaved else 0, wq, wk, eps,
+            pqo, *(none if q is None else _head_strides(q_out)),
+            pko, *(none if k is None else _head_strides(k_out)), s),
+            "svdq_rope_qk")
+    return q_out, k_out
+
+
+def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+              cu_seqlens: Optional[torch.Tensor] = None, causal: bool = False,
+              scale: Optional[float] = None, out: Optional[torch.Tensor] = None,
+              stream=None) -> torch.Tensor:
+    """Attention over whole packed sequences -> out [T, Hq, D].
+
+    q [T, Hq, D], k, v [T, Hk, D] bf16 or fp16 (strided views allowed),
+    Hq a multiple of Hk; the sequences are the row ranges of cu_seqlens
+    [n_seqs + 1] int32 on the device (None: one), each attending within
+    itself, only backwards with causal.  scale None: 1 / sqrt(D).  Rows in
+    no sequence are left as they are in out."""
+    code = _need_16bit(q, "q", 3)
+    T, Hq, D = q.shape
+    if k.dim() != 3:
+        raise ValueError("k must have 3 dims")
+    Hk = k.shape[1]
+    dev = q.device
+    pq = _need_like(q, q, (T, Hq, D), "q")
+    pk = _need_like(k, q, (T, Hk, D), "k")
+    pv = _need_like(v, q, (T, Hk, D), "v")
+    cu, S = _need_cu(cu_seqlens, dev)
+    if scale is None:
+        scale = D ** -0.5 if D else 1.0
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty(T, Hq, D, dtype=q.dtype, device=dev)
+        po = _need_like(out, q, (T, Hq, D), "out")
+        _check(_lib.svdq_attention(code, pq, *_head_strides(q), pk, *_head_strides(k), pv,
+                                   *_head_strides(v), T, Hq, Hk, D, cu, S, 1 if causal else 0,
+                                   scale, po, *_head_strides(out), s),
+               "svdq_attention")
     return out
 
 
