@@ -406,53 +406,52 @@ _NORMS = {None: NORM_NONE, "rms": NORM_RMS, "layer": NORM_LAYER}
 
 
 class _On:
-    """The device of a call's tensors made current, and its stream: the given
-    one, or the device's current one.  Outputs allocated inside belong to
-    that stream."""
+    """The device of a call's tensors (its index) made current, and its
+    stream: the given one, or the device's current one.  Outputs allocated
+    inside belong to that stream."""
 
-    __slots__ = ("dev", "stream", "ctx")
+    __slots__ = ("index", "stream", "ctx")
 
-    def __init__(self, dev: torch.device, stream: Optional[torch.cuda.Stream]):
-        self.dev = dev
+    def __init__(self, index: int, stream: Optional[torch.cuda.Stream]):
+        self.index = index
         self.stream = stream
         self.ctx = None
         if stream is not None:
-            if stream.device != dev:
-                raise ValueError(f"stream is on {stream.device}, the tensors on {dev}")
+            if stream.device.index != index:
+                raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
             self.ctx = torch.cuda.stream(stream)       # also makes its device current
-        elif dev.index != torch.cuda.current_device():
-            self.ctx = torch.cuda.device(dev)
+        elif index != torch._C._cuda_getDevice():
+            self.ctx = torch.cuda.device(index)
 
     def __enter__(self):
         if self.ctx is not None:
             self.ctx.__enter__()
-        s = self.stream if self.stream is not None else torch.cuda.current_stream(self.dev)
-        return s.cuda_stream
+        if self.stream is not None:
+            return self.stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *exc):
         if self.ctx is not None:
             self.ctx.__exit__(*exc)
 
 
-def _need_like(t: Optional[torch.Tensor], first: torch.Tensor, shape, name: str) -> int:
-    """Check an optional operand against the call's first tensor; its address
-    (None for None)."""
-    if t is None:
-        return None
-    if t.dtype is not first.dtype or t.device != first.device:
-        raise ValueError(f"{name} must be {first.dtype} on {first.device}, "
-                         f"got {t.dtype} on {t.device}")
-    if tuple(t.shape) != shape:
+def _need_like(t: torch.Tensor, dtype: torch.dtype, index: int, shape, name: str):
+    """Check an operand against the call's type, device and shape; its
+    strides, with a last one of 1."""
+    if t.dtype is not dtype or t.get_device() != index:
+        raise ValueError(f"{name} must be {dtype} on cuda:{index}, got {t.dtype} on {t.device}")
+    if t.shape != shape:
         raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
+    strides = t.stride()
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name} must have unit stride along its last dimension")
-    return t.data_ptr()
+    return strides
 
 
 def _need_16bit(t: torch.Tensor, name: str, dim: int) -> int:
+    code = _DTYPES.get(t.dtype)
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"{name} must be bfloat16 or float16, got {t.dtype}")
     if t.dim() != dim:
@@ -460,15 +459,14 @@ def _need_16bit(t: torch.Tensor, name: str, dim: int) -> int:
     return code
 
 
-def _need_cu(cu: Optional[torch.Tensor], dev: torch.device):
-    """(address, number of sequences) of cu_seqlens."""
-    if cu is None:
-        return None, 1
-    if cu.dtype is not torch.int32 or cu.device != dev or cu.dim() != 1 or cu.shape[0] < 2:
-        raise ValueError(f"cu_seqlens must be an int32 vector of at least 2 on {dev}")
+def _need_cu(cu: torch.Tensor, index: int) -> int:
+    """The number of sequences of cu_seqlens."""
+    if (cu.dtype is not torch.int32 or cu.get_device() != index or cu.dim() != 1
+            or cu.shape[0] < 2):
+        raise ValueError(f"cu_seqlens must be an int32 vector of at least 2 on cuda:{index}")
     if not cu.is_contiguous():
         raise ValueError("cu_seqlens must be contiguous")
-    return cu.data_ptr(), cu.shape[0] - 1
+    return cu.shape[0] - 1
 
 
 def norm_gate_residual(x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
@@ -494,37 +492,53 @@ def norm_gate_residual(x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
     code = _need_16bit(x, "x", 2)
     if post not in _NORMS or pre not in _NORMS:
         raise ValueError('post and pre must be None, "rms" or "layer"')
-    T, C = x.shape
-    dev = x.device
-    px = _need_like(x, x, (T, C), "x")
-    py = _need_like(y, x, (T, C), "y")
-    cu, S = _need_cu(cu_seqlens, dev)
-    pg = _need_like(gate, x, (S, C), "gate")
-    ps = _need_like(scale, x, (S, C), "scale")
-    pb = _need_like(shift, x, (S, C), "shift")
-    pw = _need_like(post_weight, x, (C,), "post_weight")
-    qw = _need_like(pre_weight, x, (C,), "pre_weight")
-    if y is None and h is not None:
+    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    T, C = shape
+    S = 1 if cu_seqlens is None else _need_cu(cu_seqlens, index)
+    ldx = _need_like(x, dtype, index, shape, "x")[0]
+    py = pg = ps = pb = pw = qw = pn = ph = None
+    ldy = ldg = lds = ldb = ldh = ldn = 0
+    if y is not None:
+        ldy = _need_like(y, dtype, index, shape, "y")[0]
+        py = y.data_ptr()
+    elif h is not None:
         raise ValueError("h needs y (without y it is x itself)")
+    if gate is not None:
+        ldg = _need_like(gate, dtype, index, (S, C), "gate")[0]
+        pg = gate.data_ptr()
+    if scale is not None:
+        lds = _need_like(scale, dtype, index, (S, C), "scale")[0]
+        ps = scale.data_ptr()
+    if shift is not None:
+        ldb = _need_like(shift, dtype, index, (S, C), "shift")[0]
+        pb = shift.data_ptr()
+    if S == 1:                     # the stride of a dimension of one means nothing
+        ldg = lds = ldb = 0
+    if post_weight is not None:
+        _need_like(post_weight, dtype, index, (C,), "post_weight")
+        pw = post_weight.data_ptr()
+    if pre_weight is not None:
+        _need_like(pre_weight, dtype, index, (C,), "pre_weight")
+        qw = pre_weight.data_ptr()
     want_n = pre is not None or scale is not None or shift is not None
-    if n is not None and not want_n and y is None:
-        raise ValueError("nothing to compute: neither y nor pre, scale or shift")
-    with _On(dev, stream) as s:
-        if y is not None and h is None:
-            h = torch.empty(T, C, dtype=x.dtype, device=dev)
-        if want_n and n is None:
-            n = torch.empty(T, C, dtype=x.dtype, device=dev)
-        ph = _need_like(h, x, (T, C), "h")
-        pn = _need_like(n, x, (T, C), "n")
-
-        def ld(t, rows):
-            return 0 if t is None else t.stride(0) if rows > 1 else C
-
+    with _On(index, stream) as s:
+        if y is not None:
+            if h is None:
+                h = x.new_empty((T, C))
+            ldh = _need_like(h, dtype, index, shape, "h")[0]
+            ph = h.data_ptr()
+        if n is None and want_n:
+            n = x.new_empty((T, C))
+        if n is not None:
+            ldn = _need_like(n, dtype, index, shape, "n")[0]
+            pn = n.data_ptr()
+        if T == 1:
+            ldx = ldy = ldh = ldn = C
         _check(_lib.svdq_norm_gate_residual(
-            code, px, ld(x, T), py, ld(y, T), T, C, cu, S, _NORMS[post], pw,
-            GATE_NONE if gate is None else GATE_TANH if gate_tanh else GATE_LINEAR, pg,
-            ld(gate, S), residual_scale, _NORMS[pre], qw, ps, ld(scale, S), pb, ld(shift, S), eps,
-            ph, ld(h, T), pn, ld(n, T), s),
+            code, x.data_ptr(), ldx, py, ldy, T, C,
+            None if cu_seqlens is None else cu_seqlens.data_ptr(), S, _NORMS[post], pw,
+            GATE_NONE if gate is None else GATE_TANH if gate_tanh else GATE_LINEAR, pg, ldg,
+            residual_scale, _NORMS[pre], qw, ps, lds, pb, ldb, eps, ph, ldh, pn, ldn, s),
             "svdq_norm_gate_residual")
     return (x if y is None else h), n
 
@@ -542,13 +556,10 @@ class RopePlan:
         if sum(self.axes) > self.head_dim:
             raise ValueError(f"axes {self.axes} exceed the head's {self.head_dim}")
         self._axes = (ctypes.c_int * max(1, len(self.axes)))(*self.axes)
+        self._pairs = 1 if self.interleaved else 0
         self._turns = (ctypes.c_double * max(1, sum(max(0, a) for a in self.axes) // 2))()
         _check(_lib.svdq_rope_turns(self._axes, len(self.axes), self.theta, self._turns),
                "svdq_rope_turns")
-
-
-def _head_strides(t: torch.Tensor):
-    return t.stride(0), t.stride(1)
 
 
 def rope_qk(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: torch.Tensor,
@@ -565,42 +576,52 @@ def rope_qk(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: tor
     if first is None:
         raise ValueError("rope_qk needs q or k")
     code = _need_16bit(first, "q" if q is not None else "k", 3)
+    dtype, index = first.dtype, first.get_device()
     T, _, D = first.shape
-    dev = first.device
     if D != plan.head_dim:
         raise ValueError(f"heads of {D}, the plan is for {plan.head_dim}")
-    if k is not None and k.dim() != 3:
-        raise ValueError("k must have 3 dims")
-    Hq = 0 if q is None else q.shape[1]
-    Hk = 0 if k is None else k.shape[1]
     A = len(plan.axes)
-    if (positions.dtype is not torch.int32 or positions.device != dev
-            or tuple(positions.shape) != (T, A)):
-        raise ValueError(f"positions must be int32 [{T}, {A}] on {dev}")
-    if positions.stride(1) != 1 and A > 1:
+    if (positions.dtype is not torch.int32 or positions.get_device() != index
+            or positions.shape != (T, A)):
+        raise ValueError(f"positions must be int32 [{T}, {A}] on cuda:{index}")
+    ldp, one = positions.stride()
+    if one != 1 and A > 1:
         raise ValueError("positions must have unit stride along the axes")
     if (q is None and q_out is not None) or (k is None and k_out is not None):
         raise ValueError("an output without its input")
-    pq = _need_like(q, first, (T, Hq, D), "q")
-    pk = _need_like(k, first, (T, Hk, D), "k")
-    wq = _need_like(q_weight, first, (D,), "q_weight")
-    wk = _need_like(k_weight, first, (D,), "k_weight")
-    with _On(dev, stream) as s:
-        if q is not None and q_out is None:
-            q_out = torch.empty(T, Hq, D, dtype=q.dtype, device=dev)
-        if k is not None and k_out is None:
-            k_out = torch.empty(T, Hk, D, dtype=k.dtype, device=dev)
-        pqo = _need_like(q_out, first, (T, Hq, D), "q_out")
-        pko = _need_like(k_out, first, (T, Hk, D), "k_out")
-        none = (0, 0)
-        _check(_lib.svdq_rope_qk(
-            code, pq, *(none if q is None else _head_strides(q)), Hq,
-            pk, *(none if k is None else _head_strides(k)), Hk, T, D,
-            positions.data_ptr(), positions.stride(0) if T > 1 else A, plan._axes, A, plan._turns,
-            1 if plan.interleaved else 0, wq, wk, eps,
-            pqo, *(none if q is None else _head_strides(q_out)),
-            pko, *(none if k is None else _head_strides(k_out)), s),
-            "svdq_rope_qk")
+    Hq = Hk = 0
+    pq = pk = pqo = pko = wq = wk = None
+    qs = ks = qos = kos = (0, 0)
+    with _On(index, stream) as s:
+        if q is not None:
+            Hq = q.shape[1]
+            shape = (T, Hq, D)
+            qs = _need_like(q, dtype, index, shape, "q")
+            if q_out is None:
+                q_out = q.new_empty((T, Hq, D))
+            qos = _need_like(q_out, dtype, index, shape, "q_out")
+            pq, pqo = q.data_ptr(), q_out.data_ptr()
+        if k is not None:
+            if k.dim() != 3:
+                raise ValueError("k must have 3 dims")
+            Hk = k.shape[1]
+            shape = (T, Hk, D)
+            ks = _need_like(k, dtype, index, shape, "k")
+            if k_out is None:
+                k_out = k.new_empty(shape)
+            kos = _need_like(k_out, dtype, index, shape, "k_out")
+            pk, pko = k.data_ptr(), k_out.data_ptr()
+        if q_weight is not None:
+            _need_like(q_weight, dtype, index, (D,), "q_weight")
+            wq = q_weight.data_ptr()
+        if k_weight is not None:
+            _need_like(k_weight, dtype, index, (D,), "k_weight")
+            wk = k_weight.data_ptr()
+        _check(_lib.svdq_rope_qk(code, pq, qs[0], qs[1], Hq, pk, ks[0], ks[1], Hk, T, D,
+                                 positions.data_ptr(), ldp if T > 1 else A, plan._axes, A,
+                                 plan._turns, plan._pairs, wq, wk, eps, pqo, qos[0], qos[1], pko,
+                                 kos[0], kos[1], s),
+               "svdq_rope_qk")
     return q_out, k_out
 
 
@@ -616,25 +637,26 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     itself, only backwards with causal.  scale None: 1 / sqrt(D).  Rows in
     no sequence are left as they are in out."""
     code = _need_16bit(q, "q", 3)
-    T, Hq, D = q.shape
     if k.dim() != 3:
         raise ValueError("k must have 3 dims")
+    dtype, index, shape = q.dtype, q.get_device(), q.shape
+    T, Hq, D = shape
     Hk = k.shape[1]
-    dev = q.device
-    pq = _need_like(q, q, (T, Hq, D), "q")
-    pk = _need_like(k, q, (T, Hk, D), "k")
-    pv = _need_like(v, q, (T, Hk, D), "v")
-    cu, S = _need_cu(cu_seqlens, dev)
+    qs = _need_like(q, dtype, index, shape, "q")
+    ks = _need_like(k, dtype, index, (T, Hk, D), "k")
+    vs = _need_like(v, dtype, index, (T, Hk, D), "v")
+    S = 1 if cu_seqlens is None else _need_cu(cu_seqlens, index)
     if scale is None:
         scale = D ** -0.5 if D else 1.0
-    with _On(dev, stream) as s:
+    with _On(index, stream) as s:
         if out is None:
-            out = torch.empty(T, Hq, D, dtype=q.dtype, device=dev)
-        po = _need_like(out, q, (T, Hq, D), "out")
-        _check(_lib.svdq_attention(code, pq, *_head_strides(q), pk, *_head_strides(k), pv,
-                                   *_head_strides(v), T, Hq, Hk, D, cu, S, 1 if causal else 0,
-                                   scale, po, *_head_strides(out), s),
-               "svdq_attention")
+            out = q.new_empty((T, Hq, D))
+        os_ = _need_like(out, dtype, index, shape, "out")
+        _check(_lib.svdq_attention(
+            code, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
+            vs[1], T, Hq, Hk, D, None if cu_seqlens is None else cu_seqlens.data_ptr(), S,
+            1 if causal else 0, scale, out.data_ptr(), os_[0], os_[1], s),
+            "svdq_attention")
     return out
 
 
