@@ -25,7 +25,7 @@
 
 namespace svdq {
 
-// Eight 16-bit elements (a 16-byte word) <-> fp32.
+// Eight 16-bit elements (a 16-byte word) -> fp32.
 template <bool BF16>
 __device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
   const uint32_t v[4] = {w.x, w.y, w.z, w.w};
@@ -40,6 +40,15 @@ __device__ __forceinline__ void unpack8(const uint4& w, float (&f)[8]) {
       f[2 * i + 1] = t.y;
     }
   }
+}
+
+// The same as four packed pairs.
+template <bool BF16>
+__device__ __forceinline__ void unpack4x2(const uint4& w, uint64_t (&f)[4]) {
+  float t[8];
+  unpack8<BF16>(w, t);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = pk(t[2 * i], t[2 * i + 1]);
 }
 
 // Two fp32 -> a pair of 16-bit elements, nearest-even (lo in the low half).
@@ -57,6 +66,18 @@ template <bool BF16>
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(pack2<BF16>(f[0], f[1]), pack2<BF16>(f[2], f[3]), pack2<BF16>(f[4], f[5]),
                     pack2<BF16>(f[6], f[7]));
+}
+
+template <bool BF16>
+__device__ __forceinline__ uint4 pack4x2(const uint64_t (&f)[4]) {
+  uint32_t r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float lo, hi;
+    upk(f[i], lo, hi);
+    r[i] = pack2<BF16>(lo, hi);
+  }
+  return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 // 16 bytes that this kernel reads once (not kept in L1).  Plain loads, not
@@ -109,29 +130,34 @@ __device__ __forceinline__ int find_sequence(const int32_t* cu, int S, int row, 
 }
 
 // Sum over the block of one value per thread, the same in every thread and
-// every run (fixed order).  `buf` alternates so that one barrier is enough.
-__device__ __forceinline__ float block_sum(float v, float* red, int& buf, int warps) {
+// every run (fixed order).  `buf` alternates so that one barrier is enough;
+// the words of absent warps hold zero.
+__device__ __forceinline__ float block_sum(float v, float (*red)[16], int& buf, int warps) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
   if (warps == 1) return v;
-  float* r = red + 16 * buf;
+  float* r = red[buf];
   buf ^= 1;
   if ((threadIdx.x & 31) == 0) r[threadIdx.x >> 5] = v;
   __syncthreads();
-  float s = 0.f;
-#pragma unroll
-  for (int i = 0; i < MAX_THREADS / 32; ++i) s += i < warps ? r[i] : 0.f;
-  return s;
+  const ulonglong2* r2 = reinterpret_cast<const ulonglong2*>(r);
+  uint64_t s = add2(add2(r2[0].x, r2[0].y), add2(r2[1].x, r2[1].y));
+  if (warps > 8) s = add2(s, add2(add2(r2[2].x, r2[2].y), add2(r2[3].x, r2[3].y)));
+  float lo, hi;
+  upk(s, lo, hi);
+  return lo + hi;
 }
 
 template <bool BF16, int VPT>
-__global__ void __launch_bounds__(MAX_THREADS) norm_gate_kernel(const Params p) {
-  __shared__ float red[2][16];
-  griddep_wait();
-  griddep_launch_dependents();
+__global__ void __launch_bounds__(MAX_THREADS, VPT == 1 ? 2 : 1) norm_gate_kernel(const Params p) {
+  __shared__ __align__(16) float red[2][16];
   const int lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5;
   int buf = 0;
+  if (threadIdx.x < 32) red[threadIdx.x >> 4][threadIdx.x & 15] = 0.f;
+  __syncthreads();
+  griddep_wait();
+  griddep_launch_dependents();
   const int row0 = static_cast<int>(blockIdx.x) * p.rows_per_block;
   const int row1 = min(p.T, row0 + p.rows_per_block);
   if (row0 >= row1) return;
@@ -152,29 +178,57 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_gate_kernel(const Params p) 
   int seq_begin = p.cu && s < p.S ? p.cu[s] : 0;
   bool fresh = true;   // the sequence's vectors are not in registers yet
 
-  float gw[VPT][8], sw[VPT][8], sb[VPT][8];
+  // gate x post weight, pre weight x (1 + scale), shift
+  uint64_t gw[VPT][4], sw[VPT][4], sb[VPT][4];
   uint4 xv[VPT], yv[VPT];
 #pragma unroll
   for (int i = 0; i < VPT; ++i) {
     xv[i] = in[i] ? ld_stream(p.x + row0 * p.ldx + col[i]) : zero;
     yv[i] = in[i] && has_y ? ld_stream(p.y + row0 * p.ldy + col[i]) : zero;
   }
+  const uint64_t a2 = pk(p.a, p.a);
+
+  // Takes the mean off (layer norm: two passes over the registers, so that a
+  // large mean costs no digits) and returns 1 / sqrt(mean square + eps).
+  auto normalize = [&](uint64_t (&v)[VPT][4], int kind) {
+    if (kind == NORM_LAYER) {
+      uint64_t t = 0;   // (0, 0); columns behind the last one hold zeros
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) t = add2(t, add2(add2(v[i][0], v[i][1]), add2(v[i][2], v[i][3])));
+      float lo, hi;
+      upk(t, lo, hi);
+      const float m = block_sum(lo + hi, red, buf, warps) * -p.inv_c;
+#pragma unroll
+      for (int i = 0; i < VPT; ++i) {
+        const uint64_t m2 = in[i] ? pk(m, m) : 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][e] = add2(v[i][e], m2);
+      }
+    }
+    uint64_t q = 0;
+#pragma unroll
+    for (int i = 0; i < VPT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q = fma2(v[i][e], v[i][e], q);
+    float lo, hi;
+    upk(q, lo, hi);
+    return rsqrtf(fmaf(block_sum(lo + hi, red, buf, warps), p.inv_c, p.eps));
+  };
 
   for (int row = row0; row < row1; ++row) {
     while (p.cu && s < p.S && row >= seq_end) {
       ++s;
-      seq_begin = seq_end;
       if (s < p.S) {
         seq_begin = p.cu[s];
         seq_end = p.cu[s + 1];
       }
       fresh = true;
     }
-    float u[VPT][8], h[VPT][8];
+    uint64_t u[VPT][4], h[VPT][4];
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
-      unpack8<BF16>(yv[i], u[i]);
-      unpack8<BF16>(xv[i], h[i]);
+      unpack4x2<BF16>(yv[i], u[i]);
+      unpack4x2<BF16>(xv[i], h[i]);
     }
     if (row + 1 < row1) {
 #pragma unroll
@@ -191,75 +245,62 @@ __global__ void __launch_bounds__(MAX_THREADS) norm_gate_kernel(const Params p) 
       fresh = false;
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
-        if (!in[i]) continue;
-        float t[8];
+        float g[8], w[8], b[8], t[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) gw[i][e] = 1.f, sw[i][e] = 1.f, sb[i][e] = 0.f;
-        if (p.gate_kind != GATE_NONE) {
-          unpack8<BF16>(*reinterpret_cast<const uint4*>(p.gate + s * p.ldg + col[i]), t);
+        for (int e = 0; e < 8; ++e) g[e] = 1.f, w[e] = 1.f, b[e] = 0.f;
+        if (in[i]) {
+          if (p.gate_kind != GATE_NONE) {
+            unpack8<BF16>(*reinterpret_cast<const uint4*>(p.gate + s * p.ldg + col[i]), g);
+            if (p.gate_kind == GATE_TANH) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) gw[i][e] = p.gate_kind == GATE_TANH ? tanhf(t[e]) : t[e];
+              for (int e = 0; e < 8; ++e) g[e] = tanhf(g[e]);
+            }
+          }
+          if (p.post_w) {
+            unpack8<BF16>(*reinterpret_cast<const uint4*>(p.post_w + col[i]), t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] *= t[e];
+          }
+          if (p.scale) {
+            unpack8<BF16>(*reinterpret_cast<const uint4*>(p.scale + s * p.lds + col[i]), t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] += t[e];
+          }
+          if (p.pre_w) {
+            unpack8<BF16>(*reinterpret_cast<const uint4*>(p.pre_w + col[i]), t);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] *= t[e];
+          }
+          if (p.shift) unpack8<BF16>(*reinterpret_cast<const uint4*>(p.shift + s * p.ldb + col[i]), b);
         }
-        if (p.post_w) {
-          unpack8<BF16>(*reinterpret_cast<const uint4*>(p.post_w + col[i]), t);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) gw[i][e] *= t[e];
+        for (int e = 0; e < 4; ++e) {
+          gw[i][e] = pk(g[2 * e], g[2 * e + 1]);
+          sw[i][e] = pk(w[2 * e], w[2 * e + 1]);
+          sb[i][e] = pk(b[2 * e], b[2 * e + 1]);
         }
-        if (p.scale) {
-          unpack8<BF16>(*reinterpret_cast<const uint4*>(p.scale + s * p.lds + col[i]), t);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sw[i][e] = 1.f + t[e];
-        }
-        if (p.pre_w) {
-          unpack8<BF16>(*reinterpret_cast<const uint4*>(p.pre_w + col[i]), t);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sw[i][e] *= t[e];
-        }
-        if (p.shift) unpack8<BF16>(*reinterpret_cast<const uint4*>(p.shift + s * p.ldb + col[i]), sb[i]);
       }
     }
 
-    // 1 / rms of v, for the layer norm after taking the mean off (two
-    // passes over the registers, so that a large mean costs no digits).
-    auto normalize = [&](float (&v)[VPT][8], int kind) {
-      if (kind == NORM_LAYER) {
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) m += in[i] ? v[i][e] : 0.f;
-        m = block_sum(m, red[0], buf, warps) * p.inv_c;
-#pragma unroll
-        for (int i = 0; i < VPT; ++i)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[i][e] -= m;
-      }
-      float q = 0.f;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q = in[i] ? fmaf(v[i][e], v[i][e], q) : q;
-      return rsqrtf(fmaf(block_sum(q, red[0], buf, warps), p.inv_c, p.eps));
-    };
-
     if (has_y) {
       const float r = p.post == NORM_NONE ? 1.f : normalize(u, p.post);
+      const uint64_t r2 = pk(r, r);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = fmaf(p.a, h[i][e], (u[i][e] * r) * gw[i][e]);
-        if (in[i])
-          *reinterpret_cast<uint4*>(p.h + row * p.ldh + col[i]) = pack8<BF16>(h[i]);
+        for (int e = 0; e < 4; ++e) h[i][e] = fma2(mul2(u[i][e], r2), gw[i][e], mul2(h[i][e], a2));
+        if (in[i]) *reinterpret_cast<uint4*>(p.h + row * p.ldh + col[i]) = pack4x2<BF16>(h[i]);
       }
     }
     if (p.n) {
       const float r = p.pre == NORM_NONE ? 1.f : normalize(h, p.pre);
+      const uint64_t r2 = pk(r, r);
 #pragma unroll
       for (int i = 0; i < VPT; ++i) {
         if (!in[i]) continue;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) h[i][e] = fmaf(h[i][e] * r, sw[i][e], sb[i][e]);
-        *reinterpret_cast<uint4*>(p.n + row * p.ldn + col[i]) = pack8<BF16>(h[i]);
+        for (int e = 0; e < 4; ++e) h[i][e] = fma2(mul2(h[i][e], r2), sw[i][e], sb[i][e]);
+        *reinterpret_cast<uint4*>(p.n + row * p.ldn + col[i]) = pack4x2<BF16>(h[i]);
       }
     }
   }

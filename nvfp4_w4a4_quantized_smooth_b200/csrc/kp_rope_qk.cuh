@@ -57,20 +57,17 @@ __global__ void __launch_bounds__(THREADS) rope_qk_kernel(const __grid_constant_
   const int head0 = static_cast<int>(threadIdx.x) / p.lanes;
   const int heads = THREADS / p.lanes;                           // heads a pass covers
   const bool in = 8 * j < p.D;
-  const int passes = (H + heads - 1) / heads;
-  const int total = nt * passes;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 
-  auto load = [&](int i) -> uint4 {
-    const int t = i / passes, h = head0 + (i - t * passes) * heads;
-    if (i >= total || h >= H || !in) return zero;
+  auto load = [&](int t, int h) -> uint4 {
+    if (h >= H || !in) return zero;
     const uint16_t* src = h < p.Hq ? p.q + (t0 + t) * p.qst + h * p.qsh
                                    : p.k + (t0 + t) * p.kst + (h - p.Hq) * p.ksh;
     return ld_stream(src + 8 * j);
   };
   uint4 raw[UNROLL];
 #pragma unroll
-  for (int u = 0; u < UNROLL; ++u) raw[u] = load(u);
+  for (int u = 0; u < UNROLL; ++u) raw[u] = load(0, head0 + u * heads);
   uint4 wq = zero, wk = zero;
   if (in && p.qw) wq = *reinterpret_cast<const uint4*>(p.qw + 8 * j);
   if (in && p.kw) wk = *reinterpret_cast<const uint4*>(p.kw + 8 * j);
@@ -87,65 +84,85 @@ __global__ void __launch_bounds__(THREADS) rope_qk_kernel(const __grid_constant_
   }
   __syncthreads();
 
-  const int quarter = p.half / 8;   // words of the lower half (halves layout)
-  for (int i0 = 0; i0 < total; i0 += UNROLL) {
-    uint4 cur[UNROLL];
+  // Lanes of this head, for its sum of squares.
+  const uint32_t group = p.lanes == 32 ? 0xFFFFFFFFu
+                                       : ((1u << p.lanes) - 1u) << (threadIdx.x & 31 & ~(p.lanes - 1));
+  // The halves layout: the partner word, `words` up or down, is another lane's.
+  const int words = p.half / 8;
+  const bool low = j < words;
+  const int from = (threadIdx.x & 31 & ~(p.lanes - 1)) + (low ? j + words : j < 2 * words ? j - words : j);
+  const float sign = low ? -1.f : 1.f;
+
+  for (int t = 0; t < nt; ++t) {
+    // This lane's cosines and sines: the same for every head of the token.
+    float c[8], sn[8];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      cur[u] = raw[u];
-      raw[u] = load(i0 + UNROLL + u);
+    for (int e = 0; e < 8; ++e) {
+      const int i = p.pairs ? 4 * j + (e >> 1) : 8 * (low ? j : j - words) + e;
+      const bool turned = p.pairs ? i < p.half : j < 2 * words;
+      const float2 v = turned ? cs[t][i] : make_float2(1.f, 0.f);
+      c[e] = v.x;
+      sn[e] = p.pairs ? ((e & 1) ? v.y : -v.y) : sign * v.y;
     }
+    for (int h0 = head0; h0 < H; h0 += UNROLL * heads) {
+      uint4 cur[UNROLL];
+      const bool next_token = h0 + UNROLL * heads >= H;
+      const int nh = next_token ? head0 : h0 + UNROLL * heads;
+      const int tn = next_token ? t + 1 : t;
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u) {
-      const int i = i0 + u;
-      if (i >= total) break;
-      const int t = i / passes, h = head0 + (i - t * passes) * heads;
-      const bool is_q = h < p.Hq;
-      float v[8];
-      unpack8<BF16>(cur[u], v);
-      if (is_q ? p.qw != nullptr : p.kw != nullptr) {
-        float w[8], q = 0.f;
-        unpack8<BF16>(is_q ? wq : wk, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
-        // lanes of one head: a group of p.lanes (all of the warp's lanes
-        // with the same head take this branch together)
-        const uint32_t mask = p.lanes == 32 ? 0xFFFFFFFFu
-                                            : ((1u << p.lanes) - 1u) << (threadIdx.x & 31 & ~(p.lanes - 1));
-        for (int o = p.lanes / 2; o > 0; o >>= 1) q += __shfl_xor_sync(mask, q, o);
-        const float r = rsqrtf(fmaf(q, p.inv_d, p.eps));
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = (v[e] * r) * w[e];
+      for (int u = 0; u < UNROLL; ++u) {
+        cur[u] = raw[u];
+        if (tn < nt) raw[u] = load(tn, nh + u * heads);
       }
-      float o[8];
-      if (p.pairs) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const bool turned = 4 * j + e < p.half;
-          const float2 c = turned ? cs[t][4 * j + e] : make_float2(1.f, 0.f);
-          o[2 * e] = turned ? v[2 * e] * c.x - v[2 * e + 1] * c.y : v[2 * e];
-          o[2 * e + 1] = turned ? v[2 * e] * c.y + v[2 * e + 1] * c.x : v[2 * e + 1];
-        }
-      } else {
-        // the partner word: quarter words up or down, in another lane
-        const bool low = j < quarter, turned = j < 2 * quarter;
-        const int base = threadIdx.x & 31 & ~(p.lanes - 1);
-        const int from = base + (turned ? (low ? j + quarter : j - quarter) : j);
+      for (int u = 0; u < UNROLL; ++u) {
+        const int h = h0 + u * heads;
+        if (h >= H) break;
+        const bool is_q = h < p.Hq;
+        float v[8];
+        unpack8<BF16>(cur[u], v);
+        if (is_q ? p.qw != nullptr : p.kw != nullptr) {
+          float w[8];
+          unpack8<BF16>(is_q ? wq : wk, w);
+          uint64_t q2 = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float other = __shfl_sync(0xFFFFFFFFu, v[e], from);
-          const float2 c = turned ? cs[t][8 * (low ? j : j - quarter) + e] : make_float2(1.f, 0.f);
-          o[e] = low ? v[e] * c.x - other * c.y : v[e] * c.x + other * c.y;
-        }
-        if (!turned) {
+          for (int e = 0; e < 4; ++e) {
+            const uint64_t x = pk(v[2 * e], v[2 * e + 1]);
+            q2 = fma2(x, x, q2);
+          }
+          float lo, hi;
+          upk(q2, lo, hi);
+          float q = lo + hi;
+          for (int o = p.lanes / 2; o > 0; o >>= 1) q += __shfl_xor_sync(group, q, o);
+          const float r = rsqrtf(fmaf(q, p.inv_d, p.eps));
+          const uint64_t r2 = pk(r, r);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) o[e] = v[e];
+          for (int e = 0; e < 4; ++e)
+            upk(mul2(mul2(pk(v[2 * e], v[2 * e + 1]), r2), pk(w[2 * e], w[2 * e + 1])), v[2 * e],
+                v[2 * e + 1]);
         }
-      }
-      if (in && h < H) {
-        uint16_t* dst = is_q ? p.qo + (t0 + t) * p.qost + h * p.qosh
-                             : p.ko + (t0 + t) * p.kost + (h - p.Hq) * p.kosh;
-        *reinterpret_cast<uint4*>(dst + 8 * j) = pack8<BF16>(o);
+        float o[8];
+        if (p.pairs) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[e] = fmaf(v[e ^ 1], sn[e], v[e] * c[e]);
+          // Past the rotated part: as it is, whatever the neighbour holds.
+          if (4 * j + 4 > p.half) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              if (4 * j + (e >> 1) >= p.half) o[e] = v[e];
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float other = __shfl_sync(group, v[e], from);
+            o[e] = j < 2 * words ? fmaf(other, sn[e], v[e] * c[e]) : v[e];
+          }
+        }
+        if (in) {
+          uint16_t* dst = is_q ? p.qo + (t0 + t) * p.qost + h * p.qosh
+                               : p.ko + (t0 + t) * p.kost + (h - p.Hq) * p.kosh;
+          *reinterpret_cast<uint4*>(dst + 8 * j) = pack8<BF16>(o);
+        }
       }
     }
   }
