@@ -149,7 +149,7 @@ __device__ __forceinline__ float block_sum(float v, float (*red)[16], int& buf, 
 }
 
 template <bool BF16, int VPT>
-__global__ void __launch_bounds__(MAX_THREADS, VPT == 1 ? 2 : 1) norm_gate_kernel(const Params p) {
+__global__ void __launch_bounds__(VPT == 1 ? 256 : MAX_THREADS, VPT == 1 ? 4 : 1) norm_gate_kernel(const Params p) {
   __shared__ __align__(16) float red[2][16];
   const int lane = threadIdx.x & 31;
   const int warps = blockDim.x >> 5;

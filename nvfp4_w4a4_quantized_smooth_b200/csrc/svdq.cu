@@ -1073,6 +1073,19 @@ cudaError_t launch_kn(cudaLaunchConfig_t& cfg, int vpt, const svdq::kn::Params& 
                   : cudaLaunchKernelEx(&cfg, norm_gate_kernel<BF16, 2>, p);
 }
 
+template <bool BF16>
+cudaError_t launch_kp(cudaLaunchConfig_t& cfg, bool pairs, const svdq::kp::Params& p) {
+  using namespace svdq::kp;
+  if (p.D <= 64)
+    return pairs ? cudaLaunchKernelEx(&cfg, rope_qk_kernel<BF16, 8, true>, p)
+                 : cudaLaunchKernelEx(&cfg, rope_qk_kernel<BF16, 8, false>, p);
+  if (p.D <= 128)
+    return pairs ? cudaLaunchKernelEx(&cfg, rope_qk_kernel<BF16, 16, true>, p)
+                 : cudaLaunchKernelEx(&cfg, rope_qk_kernel<BF16, 16, false>, p);
+  return pairs ? cudaLaunchKernelEx(&cfg, rope_qk_kernel<BF16, 32, true>, p)
+               : cudaLaunchKernelEx(&cfg, rope_qk_kernel<BF16, 32, false>, p);
+}
+
 template <bool BF16, int NB>
 int prepare_ka() {
   using namespace svdq::ka;
@@ -1160,10 +1173,11 @@ int svdq_norm_gate_residual(int dtype, const uint16_t* x, int64_t ldx, const uin
   p.a = residual_scale, p.eps = eps, p.inv_c = 1.f / static_cast<float>(C);
   // 8-element words per thread: as many threads as words up to 512.
   const int words = C / 8;
-  const int vpt = words <= svdq::kn::MAX_THREADS ? 1 : 2;
+  const int vpt = words <= 256 ? 1 : 2;
   const int threads = ((words + vpt - 1) / vpt + 31) / 32 * 32;
   // As many blocks as run at once (by threads), each with its run of rows.
-  const int blocks = d->num_sms * (1024 / threads > 8 ? 8 : 1024 / threads);
+  const int per_sm = (vpt == 1 ? 1024 : 512) / threads;
+  const int blocks = d->num_sms * (per_sm > 8 ? 8 : per_sm);
   p.rows_per_block = (T + blocks - 1) / blocks;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
@@ -1257,9 +1271,6 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
   p.qost = qo_stride_t, p.qosh = qo_stride_h, p.kost = ko_stride_t, p.kosh = ko_stride_h;
   p.ldpos = ld_pos;
   p.T = T, p.Hq = Hq, p.Hk = Hk, p.D = D, p.half = R / 2, p.axes = n_axes;
-  p.lanes = 1;
-  while (p.lanes < D / 8) p.lanes *= 2;
-  p.pairs = interleaved ? 1 : 0;
   p.eps = eps, p.inv_d = 1.f / static_cast<float>(D);
   int at = 0;
   for (int a = 0; a < n_axes; ++a) {
@@ -1275,9 +1286,8 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   pdl_config(&cfg, &attr, (T + p.tokens - 1) / p.tokens, svdq::kp::THREADS, 0, stream);
-  const cudaError_t e = dtype == SVDQ_BF16
-                            ? cudaLaunchKernelEx(&cfg, svdq::kp::rope_qk_kernel<true>, p)
-                            : cudaLaunchKernelEx(&cfg, svdq::kp::rope_qk_kernel<false>, p);
+  const cudaError_t e = dtype == SVDQ_BF16 ? launch_kp<true>(cfg, interleaved != 0, p)
+                                           : launch_kp<false>(cfg, interleaved != 0, p);
   if (e != cudaSuccess) return SVDQ_ERR_CUDA;
   return launch_status();
 }
