@@ -46,7 +46,6 @@ struct Params {
 template <bool BF16, int LANES, bool PAIRS>
 __global__ void __launch_bounds__(THREADS, 4) rope_qk_kernel(const __grid_constant__ Params p) {
   constexpr int HEADS = THREADS / LANES;   // heads a pass of the block covers
-  constexpr int UNROLL = 2;                // words in flight per thread
   // cos and sin of pair i of token t at [t][i].
   __shared__ __align__(16) float2 cs[MAX_TOKENS][MAX_D / 2];
   griddep_wait();
@@ -55,8 +54,6 @@ __global__ void __launch_bounds__(THREADS, 4) rope_qk_kernel(const __grid_consta
   const int nt = min(p.tokens, p.T - t0);
   const int j = static_cast<int>(threadIdx.x) % LANES;   // word of the head
   const int head0 = static_cast<int>(threadIdx.x) / LANES;
-  const bool in = 8 * j < p.D;
-  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
 
   for (int i = threadIdx.x; i < nt * p.half; i += THREADS) {
     const int t = i / p.half, c = i - t * p.half;
@@ -70,87 +67,106 @@ __global__ void __launch_bounds__(THREADS, 4) rope_qk_kernel(const __grid_consta
   }
   __syncthreads();
 
-  // Lanes of this head, for its sum of squares and its other half.
+  // Lanes of this head, for its sum of squares.
   const uint32_t group = LANES == 32 ? 0xFFFFFFFFu
                                      : ((1u << (LANES & 31)) - 1u) << (threadIdx.x & 31 & ~(LANES - 1));
-  // The halves layout: the partner word, `words` up or down, is another lane's.
-  const int words = p.half / 8;
-  const bool low = j < words;
-  const bool turned = j < 2 * words;   // halves: a whole word is, or is not
-  const int from = (threadIdx.x & 31 & ~(LANES - 1)) + (low ? j + words : turned ? j - words : j);
-  const float sign = low ? -1.f : 1.f;
+  // The lane's eight elements: pairs 4 j .. 4 j + 3, which are eight in a row,
+  // or (halves) four in a row at `lo` and their partners at `hi`; from the
+  // rotated part's end on, eight in a row.
+  const bool turned = PAIRS || 4 * j < p.half;
+  const int lo = PAIRS ? 8 * j : turned ? 4 * j : 2 * p.half + 8 * (j - p.half / 4);
+  const int hi = PAIRS ? 8 * j + 4 : turned ? 4 * j + p.half : lo + 4;
+  const bool in = lo < p.D;
 
-  // One tensor's heads of one token.
-  auto rotate = [&](const uint16_t* src, int64_t sh, uint16_t* dst, int64_t dh, int H, bool norm,
-                    const uint4& wv, const float (&c)[PAIRS ? 4 : 8], const float (&sn)[PAIRS ? 4 : 8]) {
-    src += head0 * sh + 8 * j;
-    dst += head0 * dh + 8 * j;
-    for (int h = head0; h < H; h += UNROLL * HEADS) {
-      uint4 raw[UNROLL];
+  auto load = [&](const uint16_t* src) {
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (PAIRS) {
+      v = ld_stream(src + lo);
+    } else {
+      const uint2 a = *reinterpret_cast<const uint2*>(src + lo), b = *reinterpret_cast<const uint2*>(src + hi);
+      v = make_uint4(a.x, a.y, b.x, b.y);
+    }
+    return v;
+  };
+
+  // One head: its norm, its rotation, its store.
+  auto rotate = [&](const uint4& raw, uint16_t* dst, bool norm, const uint4& wv, const float (&c)[4],
+                    const float (&sn)[4]) {
+    float v[8], o[8];
+    unpack8<BF16>(raw, v);
+    if (norm) {
+      float q = 0.f;
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        raw[u] = in && h + u * HEADS < H ? ld_stream(src) : zero;
-        src += HEADS * sh;
-      }
+      for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        if (h + u * HEADS >= H) return;
-        float v[8];
-        unpack8<BF16>(raw[u], v);
-        if (norm) {
-          float q = 0.f;
+      for (int o = LANES / 2; o > 0; o >>= 1) q += __shfl_xor_sync(group, q, o);
+      const float r = rsqrtf(fmaf(q, p.inv_d, p.eps));
+      float w[8];
+      unpack8<BF16>(wv, w);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) q = fmaf(v[e], v[e], q);
+      for (int e = 0; e < 8; ++e) v[e] = (v[e] * r) * w[e];
+    }
 #pragma unroll
-          for (int o = LANES / 2; o > 0; o >>= 1) q += __shfl_xor_sync(group, q, o);
-          const float r = rsqrtf(fmaf(q, p.inv_d, p.eps));
-          float w[8];
-          unpack8<BF16>(wv, w);
+    for (int e = 0; e < 4; ++e) {
+      constexpr int STEP = PAIRS ? 2 : 1, OTHER = PAIRS ? 1 : 4;
+      const float e0 = v[STEP * e], e1 = v[STEP * e + OTHER];
+      o[STEP * e] = fmaf(-e1, sn[e], e0 * c[e]);
+      o[STEP * e + OTHER] = fmaf(e0, sn[e], e1 * c[e]);
+    }
+    // Past the rotated part: as it is, whatever the neighbour holds.
+    if (4 * j + 4 > p.half) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) v[e] = (v[e] * r) * w[e];
-        }
-        float o[8];
-        if (PAIRS) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            o[2 * e] = fmaf(-v[2 * e + 1], sn[e], v[2 * e] * c[e]);
-            o[2 * e + 1] = fmaf(v[2 * e], sn[e], v[2 * e + 1] * c[e]);
-          }
-          // Past the rotated part: as it is, whatever the neighbour holds.
-          if (4 * j + 4 > p.half) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (4 * j + (e >> 1) >= p.half) o[e] = v[e];
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float other = __shfl_sync(group, v[e], from);
-            o[e] = turned ? fmaf(other, sn[e % (PAIRS ? 4 : 8)], v[e] * c[e % (PAIRS ? 4 : 8)]) : v[e];
-          }
-        }
-        if (in) *reinterpret_cast<uint4*>(dst) = pack8<BF16>(o);
-        dst += HEADS * dh;
-      }
+      for (int e = 0; e < 8; ++e)
+        if (4 * j + (PAIRS ? e >> 1 : e & 3) >= p.half) o[e] = v[e];
+    }
+    if (!in) return;
+    const uint4 w = pack8<BF16>(o);
+    if (PAIRS) {
+      *reinterpret_cast<uint4*>(dst + lo) = w;
+    } else {
+      *reinterpret_cast<uint2*>(dst + lo) = make_uint2(w.x, w.y);
+      *reinterpret_cast<uint2*>(dst + hi) = make_uint2(w.z, w.w);
     }
   };
 
-  uint4 wq = zero, wk = zero;
-  if (in && p.qw) wq = *reinterpret_cast<const uint4*>(p.qw + 8 * j);
-  if (in && p.kw) wk = *reinterpret_cast<const uint4*>(p.kw + 8 * j);
+  const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+  const uint4 wq = in && p.qw ? load(p.qw) : zero, wk = in && p.kw ? load(p.kw) : zero;
   for (int t = 0; t < nt; ++t) {
     // This lane's cosines and sines: the same for every head of the token.
-    float c[PAIRS ? 4 : 8], sn[PAIRS ? 4 : 8];
+    float c[4], sn[4];
 #pragma unroll
-    for (int e = 0; e < (PAIRS ? 4 : 8); ++e) {
-      const int i = PAIRS ? 4 * j + e : 8 * (low ? j : j - words) + e;
-      const float2 v = (PAIRS ? i < p.half : turned) ? cs[t][i] : make_float2(1.f, 0.f);
+    for (int e = 0; e < 4; ++e) {
+      const float2 v = 4 * j + e < p.half ? cs[t][4 * j + e] : make_float2(1.f, 0.f);
       c[e] = v.x;
-      sn[e] = PAIRS ? v.y : sign * v.y;
+      sn[e] = v.y;
     }
     const int64_t row = t0 + t;
-    rotate(p.q + row * p.qst, p.qsh, p.qo + row * p.qost, p.qosh, p.Hq, p.qw != nullptr, wq, c, sn);
-    rotate(p.k + row * p.kst, p.ksh, p.ko + row * p.kost, p.kosh, p.Hk, p.kw != nullptr, wk, c, sn);
+    const uint16_t* q = p.q + row * p.qst + head0 * p.qsh;
+    const uint16_t* k = p.k + row * p.kst + head0 * p.ksh;
+    uint16_t* qo = p.qo + row * p.qost + head0 * p.qosh;
+    uint16_t* ko = p.ko + row * p.kost + head0 * p.kosh;
+    // Two heads of q and two of k in flight.
+    for (int h = head0; h < max(p.Hq, p.Hk); h += 2 * HEADS) {
+      uint4 a[2], b[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        a[u] = in && h + u * HEADS < p.Hq ? load(q) : zero;
+        b[u] = in && h + u * HEADS < p.Hk ? load(k) : zero;
+        q += HEADS * p.qsh;
+        k += HEADS * p.ksh;
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        if (h + u * HEADS < p.Hq) {
+          rotate(a[u], qo, p.qw != nullptr, wq, c, sn);
+        }
+        if (h + u * HEADS < p.Hk) {
+          rotate(b[u], ko, p.kw != nullptr, wk, c, sn);
+        }
+        qo += HEADS * p.qosh;
+        ko += HEADS * p.kosh;
+      }
+    }
   }
 }
 

@@ -9,6 +9,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
+#include <cstdlib>
 #include <mutex>
 
 #include "svdq.h"
@@ -38,9 +39,9 @@ struct DeviceInfo {
   int ks_clusters[9];
   // Max co-resident CTA pairs of the pair GEMM; -1 = not queried yet.
   int kg2_pairs = -1;
-  // The attention kernels have been given their shared memory and have the
-  // registers their warp roles share out.
-  bool ka_ready = false;
+  // The kernels between the linears have been given their shared memory, and
+  // the attention kernels have the registers their warp roles share out.
+  bool block_ready = false;
 };
 
 std::mutex g_mu;
@@ -1100,15 +1101,28 @@ int prepare_ka() {
                                                                           : SVDQ_ERR_UNSUPPORTED;
 }
 
-int ka_setup(DeviceInfo* d) {
+template <bool BF16, int VPT>
+int prepare_kn() {
+  using namespace svdq::kn;
+  return cudaFuncSetAttribute(norm_gate_kernel<BF16, VPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              ring_bytes(VPT * 8 * (VPT == 1 ? 256 : MAX_THREADS), true)) == cudaSuccess
+             ? SVDQ_OK
+             : SVDQ_ERR_CUDA;
+}
+
+int block_setup(DeviceInfo* d) {
   std::lock_guard<std::mutex> lock(g_mu);
-  if (d->ka_ready) return SVDQ_OK;
-  int st = prepare_ka<true, 1>();
+  if (d->block_ready) return SVDQ_OK;
+  int st = prepare_kn<true, 1>();
+  if (!st) st = prepare_kn<true, 2>();
+  if (!st) st = prepare_kn<false, 1>();
+  if (!st) st = prepare_kn<false, 2>();
+  if (!st) st = prepare_ka<true, 1>();
   if (!st) st = prepare_ka<true, 2>();
   if (!st) st = prepare_ka<false, 1>();
   if (!st) st = prepare_ka<false, 2>();
   if (st) return st;
-  d->ka_ready = true;
+  d->block_ready = true;
   return SVDQ_OK;
 }
 
@@ -1163,6 +1177,7 @@ int svdq_norm_gate_residual(int dtype, const uint16_t* x, int64_t ldx, const uin
     if (v.base && ((y && may_meet(eh, v)) || (n && may_meet(en, v)))) return SVDQ_ERR_INVALID_ARG;
   DeviceInfo* d = nullptr;
   if (int st = device_setup(&d)) return st;
+  if (int st = block_setup(d)) return st;
 
   svdq::kn::Params p;
   p.x = x, p.y = y, p.gate = gate, p.scale = scale, p.shift = shift;
@@ -1171,18 +1186,20 @@ int svdq_norm_gate_residual(int dtype, const uint16_t* x, int64_t ldx, const uin
   p.ldg = ld_gate, p.lds = ld_scale, p.ldb = ld_shift;
   p.T = T, p.C = C, p.S = n_seqs, p.post = post, p.pre = pre, p.gate_kind = gate_kind;
   p.a = residual_scale, p.eps = eps, p.inv_c = 1.f / static_cast<float>(C);
-  // 8-element words per thread: as many threads as words up to 512.
+  cudaLaunchConfig_t cfg;
+  cudaLaunchAttribute attr;
+  cudaError_t e;
   const int words = C / 8;
+  // 8-element words per thread: as many threads as words up to 512.
   const int vpt = words <= 256 ? 1 : 2;
   const int threads = ((words + vpt - 1) / vpt + 31) / 32 * 32;
   // As many blocks as run at once (by threads), each with its run of rows.
   const int per_sm = (vpt == 1 ? 1024 : 512) / threads;
   const int blocks = d->num_sms * (per_sm > 8 ? 8 : per_sm);
   p.rows_per_block = (T + blocks - 1) / blocks;
-  cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr;
-  pdl_config(&cfg, &attr, (T + p.rows_per_block - 1) / p.rows_per_block, threads, 0, stream);
-  const cudaError_t e = dtype == SVDQ_BF16 ? launch_kn<true>(cfg, vpt, p) : launch_kn<false>(cfg, vpt, p);
+  pdl_config(&cfg, &attr, (T + p.rows_per_block - 1) / p.rows_per_block, threads,
+             svdq::kn::ring_bytes(C, y != nullptr), stream);
+  e = dtype == SVDQ_BF16 ? launch_kn<true>(cfg, vpt, p) : launch_kn<false>(cfg, vpt, p);
   if (e != cudaSuccess) return SVDQ_ERR_CUDA;
   return launch_status();
 }
@@ -1282,6 +1299,8 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
   // Tokens per block: enough that every thread has an angle to compute and
   // several words in flight, while the blocks still fill the device.
   p.tokens = svdq::kp::MAX_TOKENS;
+  static const int kTok = getenv("ROPETOK") ? atoi(getenv("ROPETOK")) : 4;
+  p.tokens = kTok;
   while (p.tokens > 1 && (T + p.tokens - 1) / p.tokens < 4 * d->num_sms) p.tokens /= 2;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
@@ -1333,7 +1352,7 @@ int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_s
   if (may_meet(eo, eq) || may_meet(eo, ek) || may_meet(eo, ev)) return SVDQ_ERR_INVALID_ARG;
   DeviceInfo* d = nullptr;
   if (int st = device_setup(&d)) return st;
-  if (int st = ka_setup(d)) return st;
+  if (int st = block_setup(d)) return st;
 
   namespace ka = svdq::ka;
   const CUtensorMapDataType dt =
