@@ -9,7 +9,6 @@
 #include <cmath>
 #include <cstdint>
 #include <cstring>
-#include <cstdlib>
 #include <mutex>
 
 #include "svdq.h"
@@ -1074,17 +1073,14 @@ cudaError_t launch_kn(cudaLaunchConfig_t& cfg, int vpt, const svdq::kn::Params& 
                   : cudaLaunchKernelEx(&cfg, norm_gate_kernel<BF16, 2>, p);
 }
 
+using RopeKernel = void (*)(const svdq::kp::Params);
+
 template <bool BF16>
-cudaError_t launch_kp(cudaLaunchConfig_t& cfg, bool pairs, const svdq::kp::Params& p) {
+RopeKernel rope_kernel(int D, bool pairs) {
   using namespace svdq::kp;
-  if (p.D <= 64)
-    return pairs ? cudaLaunchKernelEx(&cfg, rope_qk_kernel<BF16, 8, true>, p)
-                 : cudaLaunchKernelEx(&cfg, rope_qk_kernel<BF16, 8, false>, p);
-  if (p.D <= 128)
-    return pairs ? cudaLaunchKernelEx(&cfg, rope_qk_kernel<BF16, 16, true>, p)
-                 : cudaLaunchKernelEx(&cfg, rope_qk_kernel<BF16, 16, false>, p);
-  return pairs ? cudaLaunchKernelEx(&cfg, rope_qk_kernel<BF16, 32, true>, p)
-               : cudaLaunchKernelEx(&cfg, rope_qk_kernel<BF16, 32, false>, p);
+  if (D <= 64) return pairs ? rope_qk_kernel<BF16, 8, true> : rope_qk_kernel<BF16, 8, false>;
+  if (D <= 128) return pairs ? rope_qk_kernel<BF16, 16, true> : rope_qk_kernel<BF16, 16, false>;
+  return pairs ? rope_qk_kernel<BF16, 32, true> : rope_qk_kernel<BF16, 32, false>;
 }
 
 template <bool BF16, int NB>
@@ -1110,10 +1106,21 @@ int prepare_kn() {
              : SVDQ_ERR_CUDA;
 }
 
+int prepare_kp() {
+  for (int D : {64, 128, 256})
+    for (bool pairs : {false, true})
+      for (RopeKernel k : {rope_kernel<false>(D, pairs), rope_kernel<true>(D, pairs)})
+        if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 svdq::kp::SMEM_BYTES) != cudaSuccess)
+          return SVDQ_ERR_CUDA;
+  return SVDQ_OK;
+}
+
 int block_setup(DeviceInfo* d) {
   std::lock_guard<std::mutex> lock(g_mu);
   if (d->block_ready) return SVDQ_OK;
-  int st = prepare_kn<true, 1>();
+  int st = prepare_kp();
+  if (!st) st = prepare_kn<true, 1>();
   if (!st) st = prepare_kn<true, 2>();
   if (!st) st = prepare_kn<false, 1>();
   if (!st) st = prepare_kn<false, 2>();
@@ -1280,6 +1287,7 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
       return SVDQ_ERR_INVALID_ARG;
   DeviceInfo* d = nullptr;
   if (int st = device_setup(&d)) return st;
+  if (int st = block_setup(d)) return st;
 
   svdq::kp::Params p;
   std::memset(&p, 0, sizeof(p));
@@ -1296,17 +1304,33 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
   }
   p.first[n_axes] = at;
   std::memcpy(p.turns, turns, sizeof(double) * at);
-  // Tokens per block: enough that every thread has an angle to compute and
-  // several words in flight, while the blocks still fill the device.
-  p.tokens = svdq::kp::MAX_TOKENS;
-  static const int kTok = getenv("ROPETOK") ? atoi(getenv("ROPETOK")) : 4;
-  p.tokens = kTok;
-  while (p.tokens > 1 && (T + p.tokens - 1) / p.tokens < 4 * d->num_sms) p.tokens /= 2;
+  // A unit: heads of one tensor and token, at most 4 KB of them, in whole
+  // passes of a warp; each warp has a run of units, three blocks per SM.
+  const int most = static_cast<int>(svdq::kp::UNIT_BYTES) / (2 * D);
+  const int pass = D <= 64 ? 4 : D <= 128 ? 2 : 1;
+  auto split = [&](int H, int* heads) {
+    if (H == 0) return *heads = 0;
+    const int parts = (H + most - 1) / most;
+    *heads = ((H + parts - 1) / parts + pass - 1) / pass * pass;
+    if (*heads > most) *heads = most;
+    return (H + *heads - 1) / *heads;
+  };
+  p.parts_q = split(Hq, &p.heads_q);
+  p.parts = p.parts_q + split(Hk, &p.heads_k);
+  const int64_t units = static_cast<int64_t>(T) * p.parts;
+  const int64_t warps = static_cast<int64_t>(3) * d->num_sms * svdq::kp::WARPS;
+  const int64_t per_warp = (units + warps - 1) / warps;
+  if (per_warp > INT_MAX) return SVDQ_ERR_UNSUPPORTED;
+  p.units_per_warp = static_cast<int>(per_warp);
+  const int64_t per_block = per_warp * svdq::kp::WARPS;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
-  pdl_config(&cfg, &attr, (T + p.tokens - 1) / p.tokens, svdq::kp::THREADS, 0, stream);
-  const cudaError_t e = dtype == SVDQ_BF16 ? launch_kp<true>(cfg, interleaved != 0, p)
-                                           : launch_kp<false>(cfg, interleaved != 0, p);
+  pdl_config(&cfg, &attr, static_cast<unsigned>((units + per_block - 1) / per_block),
+             svdq::kp::THREADS, svdq::kp::SMEM_BYTES, stream);
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, dtype == SVDQ_BF16 ? rope_kernel<true>(D, interleaved != 0)
+                                                  : rope_kernel<false>(D, interleaved != 0),
+                         p);
   if (e != cudaSuccess) return SVDQ_ERR_CUDA;
   return launch_status();
 }
