@@ -50,6 +50,7 @@ constexpr uint32_t BOX_BYTES = ROWS * 128;   // 128 rows x 64 elements, 128-byte
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_S = 0;            // S / P of slot s at 128 s
 constexpr uint32_t TM_O = 256;          // O of slot s at 256 + 128 s
+constexpr int P_STEPS = 6;              // 16-key steps of P that are handed over first
 constexpr float RESCALE_LOG2 = 8.f;
 // Registers per thread of the softmax warps and of the others.
 constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 80;
@@ -63,8 +64,8 @@ struct Shape {
   static constexpr uint32_t OFF_KV = 2 * TILE_BYTES;
   static constexpr uint32_t OFF_BAR = OFF_KV + STAGES * TILE_BYTES;
   // full, empty, guard_go, guard_done [STAGES], q_full, q_empty, s_full[2],
-  // p_full[2], o_full[2], flags_full[2], flags_free[2], final
-  static constexpr int BARS = 4 * STAGES + 13;
+  // p_full[2], p_rest[2], o_full[2], flags_full[2], flags_free[2], final
+  static constexpr int BARS = 4 * STAGES + 15;
   // Notes of the guards, one bit per key: [item parity][guard][8 words].
   static constexpr uint32_t OFF_FLAGS = OFF_BAR + 8 * BARS;
   static constexpr uint32_t OFF_TMEM = OFF_FLAGS + 2 * 2 * 8 * 4;
@@ -189,10 +190,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   const uint32_t q_full = bar(4 * STAGES), q_empty = bar(4 * STAGES + 1);
   auto s_full = [&](int s) { return bar(4 * STAGES + 2 + s); };
   auto p_full = [&](int s) { return bar(4 * STAGES + 4 + s); };
-  auto o_full = [&](int s) { return bar(4 * STAGES + 6 + s); };
-  auto flags_full = [&](int b) { return bar(4 * STAGES + 8 + b); };
-  auto flags_free = [&](int b) { return bar(4 * STAGES + 10 + b); };
-  const uint32_t final_bar = bar(4 * STAGES + 12);
+  auto p_rest = [&](int s) { return bar(4 * STAGES + 6 + s); };
+  auto o_full = [&](int s) { return bar(4 * STAGES + 8 + s); };
+  auto flags_full = [&](int b) { return bar(4 * STAGES + 10 + b); };
+  auto flags_free = [&](int b) { return bar(4 * STAGES + 12 + b); };
+  const uint32_t final_bar = bar(4 * STAGES + 14);
   auto s_q = [&](int s) { return sb + S_::OFF_Q + s * S_::TILE_BYTES; };
   auto s_kv = [&](uint32_t s) { return sb + S_::OFF_KV + s * S_::TILE_BYTES; };
   uint32_t* flags = reinterpret_cast<uint32_t*>(smem + S_::OFF_FLAGS);
@@ -209,6 +211,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
       mbar_init(p_full(s), 4);
+      mbar_init(p_rest(s), 4);
       mbar_init(o_full(s), 1);
       mbar_init(flags_full(s), 2);
       mbar_init(flags_free(s), 8);
@@ -279,80 +282,95 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       __syncwarp();
     } else if (warp == MMA_WARP) {
       // ------------------------------------------------------------ MMA --
+      // The warp stays together (one lane issues), so that descriptors are
+      // uniform and an MMA costs an addition or two to issue: the tensor core
+      // takes 64 cycles for one.
+      const uint32_t leader = elect_one();
       const uint32_t dn = (p.D + 15) / 16 * 16;   // columns of O, and k of Q K^T
       const int dk = dn / 16;
       const uint32_t id_o = BF16 ? idesc_bf16_f32(ROWS, dn, 0, 1) : idesc_f16_f32(ROWS, dn, 0, 1);
+      const uint64_t desc_q = smem_desc(s_q(0), 16, 1024, kLayoutSwizzle128B);
+      const uint64_t desc_k = smem_desc(s_kv(0), 16, 1024, kLayoutSwizzle128B);
+      const uint64_t desc_v = smem_desc(s_kv(0), BOX_BYTES, 1024, kLayoutSwizzle128B);
+      constexpr uint64_t TILE_16 = S_::TILE_BYTES / 16;
       uint32_t kv = 0, n = 0, phases = 0;   // ring uses, items, guarded uses by stage (parity)
-      uint32_t np[2] = {0, 0};    // P tiles waited for, by slot
+      uint32_t np[2] = {0, 0};              // P tiles waited for, by slot
       bool ok = true;
+      auto wait = [&](uint32_t b, uint32_t parity, uint32_t site) {
+        return __all_sync(0xFFFFFFFFu, svdq_wait(b, parity, site)) != 0;
+      };
+      auto wait_kv = [&](uint32_t u) {
+        const bool r = wait(full_bar(u % STAGES), (u / STAGES) & 1u, SITE_MMA_KV);
+        tc_fence_after();
+        return r;
+      };
       for (int64_t w = blockIdx.x; ok && items.get(p, w, it); w += gridDim.x, ++n) {
-        if (lane == 0) {
-          const int nt[2] = {it.tiles(0, p.causal), it.tiles(1, p.causal)};
-          const int tiles = max(nt[0], nt[1]);
-          const int last = it.key_tiles() - 1;
-          const int last_steps = (it.len - last * ROWS + 15) / 16;   // 16-key steps of the last tile
-          auto qk = [&](int s, int j) {
-            const uint32_t keys = j == last ? 16 * last_steps : ROWS;
-            const uint32_t id = BF16 ? idesc_bf16_f32(ROWS, keys, 0, 0) : idesc_f16_f32(ROWS, keys, 0, 0);
-            const uint32_t kb = s_kv((kv + 2 * j) % STAGES);
-            for (int c = 0; c < dk; ++c) {
-              const uint32_t off = (c >> 2) * BOX_BYTES + 32 * (c & 3);
-              mma_f16(tmem + TM_S + ROWS * s, smem_desc(s_q(s) + off, 16, 1024, kLayoutSwizzle128B),
-                      smem_desc(kb + off, 16, 1024, kLayoutSwizzle128B), id, c != 0);
+        const int nt[2] = {it.tiles(0, p.causal), it.tiles(1, p.causal)};
+        const int tiles = max(nt[0], nt[1]);
+        const int last = it.key_tiles() - 1;
+        const int last_steps = (it.len - last * ROWS + 15) / 16;   // 16-key steps of the last tile
+        auto qk = [&](int s, int j) {
+          const uint32_t keys = j == last ? 16 * last_steps : ROWS;
+          const uint32_t id = BF16 ? idesc_bf16_f32(ROWS, keys, 0, 0) : idesc_f16_f32(ROWS, keys, 0, 0);
+          const uint64_t dq = desc_q + TILE_16 * s;
+          const uint64_t dkk = desc_k + TILE_16 * ((kv + 2 * j) % STAGES);
+#pragma unroll
+          for (int c = 0; c < 4 * NB; ++c) {
+            if (c < dk) {
+              const uint64_t off = ((c >> 2) * BOX_BYTES + 32 * (c & 3)) / 16;
+              mma_f16_by(leader, tmem + TM_S + ROWS * s, dq + off, dkk + off, id, c != 0);
             }
-            tc_commit(s_full(s));
-          };
-          auto wait_kv = [&](uint32_t u) {
-            const bool r = svdq_wait(full_bar(u % STAGES), (u / STAGES) & 1u, SITE_MMA_KV);
-            tc_fence_after();
-            return r;
-          };
-          ok = svdq_wait(q_full, n & 1u, SITE_MMA_Q) && wait_kv(kv);
-          if (ok) {
-            for (int s = 0; s < 2; ++s)
-              if (nt[s] > 0) qk(s, 0);
-            tc_commit(empty_bar(kv % STAGES));
-            if (tiles == 1) tc_commit(q_empty);
           }
-          for (int j = 0; ok && j < tiles; ++j) {
-            const uint32_t uv = kv + 2 * j + 1, uk = uv + 1;
-            const uint32_t vb = s_kv(uv % STAGES);
-            const int steps = j == last ? last_steps : ROWS / 16;
-            const bool more = j + 1 < tiles;
-            ok = wait_kv(uv);
-            if (ok && it.guarded(j, p.causal)) {
-              const uint32_t st = uv % STAGES;
-              ok = svdq_wait(guard_done(st), (phases >> st) & 1u, SITE_MMA_GUARD);
-              phases ^= 1u << st;
-            }
-            if (ok && more) ok = wait_kv(uk);
-            for (int s = 0; ok && s < 2; ++s) {
-              if (j < nt[s]) {
-                ok = svdq_wait(p_full(s), np[s]++ & 1u, SITE_MMA_P);
-                if (!ok) break;
+          tc_commit_by(leader, s_full(s));
+        };
+        ok = wait(q_full, n & 1u, SITE_MMA_Q) && wait_kv(kv);
+        if (!ok) break;
+        for (int s = 0; s < 2; ++s)
+          if (nt[s] > 0) qk(s, 0);
+        tc_commit_by(leader, empty_bar(kv % STAGES));
+        if (tiles == 1) tc_commit_by(leader, q_empty);
+        for (int j = 0; ok && j < tiles; ++j) {
+          const uint32_t uv = kv + 2 * j + 1, uk = uv + 1;
+          const uint64_t dv = desc_v + TILE_16 * (uv % STAGES);
+          const int steps = j == last ? last_steps : ROWS / 16;
+          const bool more = j + 1 < tiles;
+          ok = wait_kv(uv);
+          if (ok && it.guarded(j, p.causal)) {
+            const uint32_t st = uv % STAGES;
+            ok = wait(guard_done(st), (phases >> st) & 1u, SITE_MMA_GUARD);
+            phases ^= 1u << st;
+          }
+          if (ok && more) ok = wait_kv(uk);
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            if (ok && j < nt[s]) {
+              // The first keys of P are multiplied while the softmax warps
+              // are at the rest.
+#pragma unroll
+              for (int part = 0; part < 2; ++part) {
+                ok = ok && wait(part ? p_rest(s) : p_full(s), np[s] & 1u, SITE_MMA_P);
                 tc_fence_after();
-                for (int c = 0; c < steps; ++c)
-                  mma_f16_ts(tmem + TM_O + ROWS * s, tmem + TM_S + ROWS * s + 8 * c,
-                             smem_desc(vb + 2048 * c, BOX_BYTES, 1024, kLayoutSwizzle128B), id_o,
-                             (j | c) != 0);
-                if (j == nt[s] - 1) tc_commit(o_full(s));
+#pragma unroll
+                for (int c = part ? P_STEPS : 0; c < (part ? ROWS / 16 : P_STEPS); ++c)
+                  if (ok && c < steps)
+                    mma_f16_ts_by(leader, tmem + TM_O + ROWS * s, tmem + TM_S + ROWS * s + 8 * c,
+                                  dv + 128 * c, id_o, (j | c) != 0);
               }
-              if (j + 1 < nt[s]) qk(s, j + 1);
+              ++np[s];
+              if (ok && j == nt[s] - 1) tc_commit_by(leader, o_full(s));
             }
-            if (!ok) break;
-            tc_commit(empty_bar(uv % STAGES));
-            if (more) tc_commit(empty_bar(uk % STAGES));
-            if (j + 2 == tiles) tc_commit(q_empty);   // the last Q K^T is in flight
+            if (ok && j + 1 < nt[s]) qk(s, j + 1);
           }
-          kv += 2 * tiles;
+          if (!ok) break;
+          tc_commit_by(leader, empty_bar(uv % STAGES));
+          if (more) tc_commit_by(leader, empty_bar(uk % STAGES));
+          if (j + 2 == tiles) tc_commit_by(leader, q_empty);   // the last Q K^T is in flight
         }
-        ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
+        kv += 2 * tiles;
       }
-      if (lane == 0) {
-        // Every MMA this thread issued completes before TMEM is released.
-        tc_commit(final_bar);
-        drain_wait(final_bar, 0, 100000000ull);
-      }
+      // Every MMA issued completes before TMEM is released.
+      tc_commit_by(leader, final_bar);
+      drain_wait(final_bar, 0, 100000000ull);
       __syncwarp();
     } else {
       // --------------------------------------------------------- guards --
@@ -450,12 +468,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               for (int e = 0; e < 32; ++e)
                 if (32 * c + e >= keys) x[c][e] = 0xFF800000u;   // -inf
           }
-          float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float t[4] = {m, m, m, m};
 #pragma unroll
           for (int c = 0; c < 4; ++c)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) t[e & 3] = fmaxf(t[e & 3], __uint_as_float(x[c][e]));
-          const float top = fmaxf(m, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])));
+            for (int e = 0; e < 32; e += 2)
+              t[(e >> 1) & 3] = max3(t[(e >> 1) & 3], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
+          const float top = fmaxf(max3(t[0], t[1], t[2]), t[3]);
           if (j == 0) {
             m = top;
           } else if (__any_sync(0xFFFFFFFFu, (top - m) * sc > RESCALE_LOG2)) {
@@ -501,12 +520,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               w16[e] = pack2<BF16>(a, b);
             }
             tmem_st_32x32b_x16(tm_s + 16 * c, w16);
+            if (c >= 2) {   // P_STEPS steps of 16 keys are there, then the rest
+              tmem_st_wait();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(c == 2 ? p_full(slot) : p_rest(slot));
+            }
           }
           upk(sum2, l0, l1);
-          tmem_st_wait();
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full(slot));
         }
         if (!ok) break;
         // -------------------------------------------------------- epilogue --
