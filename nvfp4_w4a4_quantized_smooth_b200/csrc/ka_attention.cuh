@@ -9,9 +9,10 @@
 // tensor core's row count) against all key tiles of 128 they attend.  Per
 // key tile and slot: S = Q K^T into TMEM (fp32), one softmax step by the
 // slot's four warps (one thread per row, so no shuffles), P back into the
-// same TMEM columns as 16-bit values, O += P V with P read from TMEM.  While
-// one slot's warps work on their tile the tensor core runs the other slot's
-// products, and K and V tiles pass both slots from one ring in shared memory.
+// same TMEM columns as 16-bit values, O += P V with P read from TMEM.  Each
+// slot has its own warp that issues its products, so that while one slot's
+// warps work on their tile the tensor core runs the other slot's, and K and V
+// tiles pass both slots from one ring in shared memory.
 //
 // The softmax keeps a running reference m (log2 units after the scale), sum
 // and O relative to it.  O is rescaled only when a row's maximum has grown by
@@ -25,12 +26,13 @@
 // selection, so what they hold does not matter.  Values need more, since a
 // zero weight times inf or NaN is NaN: the tile behind a sequence's end
 // holds other rows, and on the causal diagonal a tile holds values that some
-// of its rows do not attend.  For these tiles alone two guard warps zero the
+// of its rows do not attend.  For these tiles alone a guard warp zeroes the
 // rows behind the end (only up to the next multiple of 16; the product stops
-// there) and, when causal, replace non-finite values by zero and note their
+// there) and, when causal, replaces non-finite values by zero and notes their
 // keys; the epilogue adds a noted value back into the rows that do attend it.
 #pragma once
 
+#include <climits>
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -44,8 +46,8 @@ namespace ka {
 constexpr int ROWS = 128;               // query rows of a slot, keys of a tile
 constexpr int ITEM_ROWS = 2 * ROWS;     // query rows of a work item
 constexpr int MAX_D = 128;
-constexpr int NUM_THREADS = 384;        // 2 x 4 softmax warps, MMA, TMA, 2 guards
-constexpr int MMA_WARP = 8, TMA_WARP = 9, GUARD_WARP = 10;
+constexpr int NUM_THREADS = 384;        // 2 x 4 softmax warps, 2 MMA, TMA, guard
+constexpr int MMA_WARP = 8, TMA_WARP = 10, GUARD_WARP = 11;
 constexpr uint32_t BOX_BYTES = ROWS * 128;   // 128 rows x 64 elements, 128-byte swizzle
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_S = 0;            // S / P of slot s at 128 s
@@ -64,11 +66,12 @@ struct Shape {
   static constexpr uint32_t OFF_KV = 2 * TILE_BYTES;
   static constexpr uint32_t OFF_BAR = OFF_KV + STAGES * TILE_BYTES;
   // full, empty, guard_go, guard_done [STAGES], q_full, q_empty, s_full[2],
-  // p_full[2], p_rest[2], o_full[2], flags_full[2], flags_free[2], final
-  static constexpr int BARS = 4 * STAGES + 15;
-  // Notes of the guards, one bit per key: [item parity][guard][8 words].
+  // p_full[2], p_rest[2], o_full[2], flags_full[2], flags_free[2], final[2],
+  // turn[2]
+  static constexpr int BARS = 4 * STAGES + 18;
+  // Notes of the guard, one bit per key: [item parity][8 words].
   static constexpr uint32_t OFF_FLAGS = OFF_BAR + 8 * BARS;
-  static constexpr uint32_t OFF_TMEM = OFF_FLAGS + 2 * 2 * 8 * 4;
+  static constexpr uint32_t OFF_TMEM = OFF_FLAGS + 2 * 8 * 4;
   static constexpr uint32_t USED = OFF_TMEM + 16;
   static constexpr uint32_t SMEM_BYTES = USED + 1024;   // 1024-byte alignment of the boxes
 };
@@ -77,7 +80,7 @@ static_assert(Shape<2>::SMEM_BYTES <= 232448 && Shape<1>::SMEM_BYTES <= 232448, 
 constexpr uint32_t SITE_TMA_Q = 0x50, SITE_TMA_KV = 0x51, SITE_MMA_Q = 0x52, SITE_MMA_KV = 0x53,
                    SITE_MMA_P = 0x54, SITE_MMA_GUARD = 0x55, SITE_SOFT_S = 0x56,
                    SITE_SOFT_O = 0x57, SITE_GUARD_V = 0x58, SITE_GUARD_FLAGS = 0x59,
-                   SITE_SOFT_FLAGS = 0x5A;
+                   SITE_SOFT_FLAGS = 0x5A, SITE_MMA_TURN = 0x5B;
 
 struct Params {
   const int32_t* cu;        // [S + 1] or NULL: one sequence of all T rows
@@ -99,8 +102,10 @@ struct Item {
     const int n = key_tiles();
     return causal ? min(n, q0 / ROWS + s + 1) : n;
   }
-  __device__ __forceinline__ bool guarded(int j, int causal) const {
-    return (causal && j >= q0 / ROWS) || ((j + 1) * ROWS > len && len % 16 != 0);
+  // The first guarded value tile: the diagonal's (and all behind it), or the
+  // last one where it ends inside 16 keys.
+  __device__ __forceinline__ int guard_from(int causal) const {
+    return causal ? q0 / ROWS : len % 16 != 0 ? key_tiles() - 1 : INT_MAX;
   }
 };
 
@@ -159,6 +164,14 @@ __device__ __forceinline__ void set_max_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// ex2 that is computed where it stands (the compiler would move it behind the
+// test of the maximum, where alone its result is used).
+__device__ __forceinline__ float ex2_here(float y) {
+  float r;
+  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
+  return r;
+}
+
 template <bool BF16>
 __device__ __forceinline__ bool is_nonfinite16(uint32_t e) {
   constexpr uint32_t m = BF16 ? 0x7F80u : 0x7C00u;
@@ -176,7 +189,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   const uint32_t sb = smem_u32(smem);
-  const int warp = threadIdx.x >> 5;
+  // (by shuffle: the compiler then knows it to be the same in all lanes)
+  const int warp = __shfl_sync(0xFFFFFFFFu, static_cast<int>(threadIdx.x >> 5), 0);
   const int lane = threadIdx.x & 31;
   auto bar = [&](int i) { return sb + S_::OFF_BAR + 8u * i; };
   auto full_bar = [&](uint32_t s) { return bar(s); };
@@ -195,6 +209,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto flags_full = [&](int b) { return bar(4 * STAGES + 10 + b); };
   auto flags_free = [&](int b) { return bar(4 * STAGES + 12 + b); };
   const uint32_t final_bar = bar(4 * STAGES + 14);
+  const uint32_t turn_bar = bar(4 * STAGES + 16);
   auto s_q = [&](int s) { return sb + S_::OFF_Q + s * S_::TILE_BYTES; };
   auto s_kv = [&](uint32_t s) { return sb + S_::OFF_KV + s * S_::TILE_BYTES; };
   uint32_t* flags = reinterpret_cast<uint32_t*>(smem + S_::OFF_FLAGS);
@@ -202,21 +217,24 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(full_bar(s), 1);
-      mbar_init(empty_bar(s), 1);
+      mbar_init(empty_bar(s), 2);   // both slots' products have passed it
       mbar_init(guard_go(s), 1);
-      mbar_init(guard_done(s), 2);
+      mbar_init(guard_done(s), 1);
     }
     mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
+    mbar_init(q_empty, 2);
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full(s), 1);
       mbar_init(p_full(s), 4);
       mbar_init(p_rest(s), 4);
       mbar_init(o_full(s), 1);
-      mbar_init(flags_full(s), 2);
+      mbar_init(flags_full(s), 1);
       mbar_init(flags_free(s), 8);
     }
     mbar_init(final_bar, 1);
+    mbar_init(final_bar + 8, 1);
+    mbar_init(turn_bar, 1);
+    mbar_init(turn_bar + 8, 1);
     fence_mbar_init();
   }
   if (warp == MMA_WARP) {
@@ -231,7 +249,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(smem + S_::OFF_TMEM);
+  const uint32_t tmem =
+      __shfl_sync(0xFFFFFFFFu, *reinterpret_cast<volatile uint32_t*>(smem + S_::OFF_TMEM), 0);
   griddep_wait();
   griddep_launch_dependents();
 
@@ -265,7 +284,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int b = 0; b < NB; ++b)
               tma_load_3d(s_kv(st) + b * BOX_BYTES, (j & 1) ? &tm_v : &tm_k, 64 * b, kh,
                           it.begin + (j >> 1) * ROWS, full_bar(st));
-            if ((j & 1) && it.guarded(j >> 1, p.causal)) mbar_arrive(guard_go(st));
+            if ((j & 1) && (j >> 1) >= it.guard_from(p.causal)) mbar_arrive(guard_go(st));
           }
         }
         ok = __shfl_sync(0xFFFFFFFFu, ok, 0);
@@ -280,106 +299,124 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         if (n > 0) drain_wait(q_full, (n - 1) & 1u, 50000000ull);
       }
       __syncwarp();
-    } else if (warp == MMA_WARP) {
+    } else if (warp != GUARD_WARP) {
       // ------------------------------------------------------------ MMA --
-      // The warp stays together (one lane issues), so that descriptors are
-      // uniform and an MMA costs an addition or two to issue: the tensor core
-      // takes 64 cycles for one.
+      // A warp per slot; they take turns at the tensor core, a slot's P V and
+      // next Q K^T at a time, which keeps the slots half a period apart (left
+      // alone they fall into step and wait for the same unit at the same
+      // time: 365 us against 285 at 4352 x 30 heads).  It stays together (one lane issues), so that
+      // descriptors are uniform and an MMA costs an addition or two to issue:
+      // the tensor core takes 64 cycles for one.
+      const int s = warp - MMA_WARP;
       const uint32_t leader = elect_one();
       const uint32_t dn = (p.D + 15) / 16 * 16;   // columns of O, and k of Q K^T
       const int dk = dn / 16;
       const uint32_t id_o = BF16 ? idesc_bf16_f32(ROWS, dn, 0, 1) : idesc_f16_f32(ROWS, dn, 0, 1);
-      const uint64_t desc_q = smem_desc(s_q(0), 16, 1024, kLayoutSwizzle128B);
+      const uint64_t desc_q = smem_desc(s_q(s), 16, 1024, kLayoutSwizzle128B);
       const uint64_t desc_k = smem_desc(s_kv(0), 16, 1024, kLayoutSwizzle128B);
       const uint64_t desc_v = smem_desc(s_kv(0), BOX_BYTES, 1024, kLayoutSwizzle128B);
-      constexpr uint64_t TILE_16 = S_::TILE_BYTES / 16;
-      uint32_t kv = 0, n = 0, phases = 0;   // ring uses, items, guarded uses by stage (parity)
-      uint32_t np[2] = {0, 0};              // P tiles waited for, by slot
+      constexpr uint32_t TILE_16 = S_::TILE_BYTES / 16;
+      const uint32_t tm_s = tmem + TM_S + ROWS * s, tm_o = tmem + TM_O + ROWS * s;
+      const uint32_t b_s = s_full(s), b_p = p_full(s), b_rest = p_rest(s), b_o = o_full(s);
+      uint32_t st = 0, ph = 0;          // next use of the ring: stage, parity
+      uint32_t guards = 0;              // parity of the guarded uses, by stage
+      uint32_t n = 0, np = 0;           // items, P tiles
+      uint32_t turn = s ^ 1u;           // parity of the turns (slot 0 has the first)
       bool ok = true;
       auto wait = [&](uint32_t b, uint32_t parity, uint32_t site) {
-        return __all_sync(0xFFFFFFFFu, svdq_wait(b, parity, site)) != 0;
+        if (!__all_sync(0xFFFFFFFFu, mbar_try_wait(b, parity)))
+          ok = __all_sync(0xFFFFFFFFu, svdq_wait(b, parity, site)) && ok;
       };
-      auto wait_kv = [&](uint32_t u) {
-        const bool r = wait(full_bar(u % STAGES), (u / STAGES) & 1u, SITE_MMA_KV);
-        tc_fence_after();
-        return r;
+      auto next = [&]() {
+        if (++st == STAGES) st = 0, ph ^= 1u;
       };
       for (int64_t w = blockIdx.x; ok && items.get(p, w, it); w += gridDim.x, ++n) {
-        const int nt[2] = {it.tiles(0, p.causal), it.tiles(1, p.causal)};
-        const int tiles = max(nt[0], nt[1]);
+        const int mine = it.tiles(s, p.causal);            // key tiles of this slot
+        const int tiles = max(it.tiles(0, p.causal), it.tiles(1, p.causal));
         const int last = it.key_tiles() - 1;
         const int last_steps = (it.len - last * ROWS + 15) / 16;   // 16-key steps of the last tile
-        auto qk = [&](int s, int j) {
-          const uint32_t keys = j == last ? 16 * last_steps : ROWS;
-          const uint32_t id = BF16 ? idesc_bf16_f32(ROWS, keys, 0, 0) : idesc_f16_f32(ROWS, keys, 0, 0);
-          const uint64_t dq = desc_q + TILE_16 * s;
-          const uint64_t dkk = desc_k + TILE_16 * ((kv + 2 * j) % STAGES);
+        const int guard_from = it.guard_from(p.causal);
+        // S of tile j from stage `at`; the other slot's turn begins while the
+        // last products are issued.
+        auto qk = [&](int j, uint32_t at, bool pass) {
+          if (j < mine) {
+            const uint32_t keys = j == last ? 16 * last_steps : ROWS;
+            const uint32_t id = BF16 ? idesc_bf16_f32(ROWS, keys, 0, 0) : idesc_f16_f32(ROWS, keys, 0, 0);
+            const uint64_t dkk = desc_k + TILE_16 * at;
 #pragma unroll
-          for (int c = 0; c < 4 * NB; ++c) {
-            if (c < dk) {
+            for (int c = 0; c < 4 * NB; ++c) {
               const uint64_t off = ((c >> 2) * BOX_BYTES + 32 * (c & 3)) / 16;
-              mma_f16_by(leader, tmem + TM_S + ROWS * s, dq + off, dkk + off, id, c != 0);
+              if (c < dk) mma_f16_by(leader, tm_s, desc_q + off, dkk + off, id, c != 0);
+              if (c == 2 * NB - 1 && pass && leader) mbar_arrive(turn_bar + 8 * (s ^ 1));
             }
+            tc_commit_by(leader, b_s);
+          } else if (pass && leader) {
+            mbar_arrive(turn_bar + 8 * (s ^ 1));
           }
-          tc_commit_by(leader, s_full(s));
+          tc_commit_by(leader, empty_bar(at));
+          if (j == tiles - 1) tc_commit_by(leader, q_empty);
         };
-        ok = wait(q_full, n & 1u, SITE_MMA_Q) && wait_kv(kv);
+        wait(q_full, n & 1u, SITE_MMA_Q);
+        wait(full_bar(st), ph, SITE_MMA_KV);
+        tc_fence_after();
         if (!ok) break;
-        for (int s = 0; s < 2; ++s)
-          if (nt[s] > 0) qk(s, 0);
-        tc_commit_by(leader, empty_bar(kv % STAGES));
-        if (tiles == 1) tc_commit_by(leader, q_empty);
-        for (int j = 0; ok && j < tiles; ++j) {
-          const uint32_t uv = kv + 2 * j + 1, uk = uv + 1;
-          const uint64_t dv = desc_v + TILE_16 * (uv % STAGES);
-          const int steps = j == last ? last_steps : ROWS / 16;
+        qk(0, st, false);
+        next();
+        for (int j = 0; j < tiles; ++j) {
+          // All that the turn's products need is there before it is taken.
+          const uint32_t sv = st;
+          const uint64_t dv = desc_v + TILE_16 * sv;
           const bool more = j + 1 < tiles;
-          ok = wait_kv(uv);
-          if (ok && it.guarded(j, p.causal)) {
-            const uint32_t st = uv % STAGES;
-            ok = wait(guard_done(st), (phases >> st) & 1u, SITE_MMA_GUARD);
-            phases ^= 1u << st;
+          wait(full_bar(sv), ph, SITE_MMA_KV);
+          if (j >= guard_from) {
+            wait(guard_done(sv), (guards >> sv) & 1u, SITE_MMA_GUARD);
+            guards ^= 1u << sv;
           }
-          if (ok && more) ok = wait_kv(uk);
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            if (ok && j < nt[s]) {
-              // The first keys of P are multiplied while the softmax warps
-              // are at the rest.
-#pragma unroll
-              for (int part = 0; part < 2; ++part) {
-                ok = ok && wait(part ? p_rest(s) : p_full(s), np[s] & 1u, SITE_MMA_P);
-                tc_fence_after();
-#pragma unroll
-                for (int c = part ? P_STEPS : 0; c < (part ? ROWS / 16 : P_STEPS); ++c)
-                  if (ok && c < steps)
-                    mma_f16_ts_by(leader, tmem + TM_O + ROWS * s, tmem + TM_S + ROWS * s + 8 * c,
-                                  dv + 128 * c, id_o, (j | c) != 0);
-              }
-              ++np[s];
-              if (ok && j == nt[s] - 1) tc_commit_by(leader, o_full(s));
-            }
-            if (ok && j + 1 < nt[s]) qk(s, j + 1);
+          next();
+          const uint32_t sk = st;
+          if (more) {
+            wait(full_bar(sk), ph, SITE_MMA_KV);
+            next();
           }
+          if (j < mine) wait(b_p, np & 1u, SITE_MMA_P);
+          wait(turn_bar + 8 * s, turn, SITE_MMA_TURN);
+          turn ^= 1u;
+          tc_fence_after();
           if (!ok) break;
-          tc_commit_by(leader, empty_bar(uv % STAGES));
-          if (more) tc_commit_by(leader, empty_bar(uk % STAGES));
-          if (j + 2 == tiles) tc_commit_by(leader, q_empty);   // the last Q K^T is in flight
+          if (j < mine) {
+            const int steps = j == last ? last_steps : ROWS / 16;
+            // The first keys of P are multiplied while the softmax warps are
+            // at the rest.
+#pragma unroll
+            for (int c = 0; c < P_STEPS; ++c)
+              if (c < steps)
+                mma_f16_ts_by(leader, tm_o, tm_s + 8 * c, dv + 128 * c, id_o, c == 0 ? j != 0 : 1u);
+            wait(b_rest, np++ & 1u, SITE_MMA_P);
+            tc_fence_after();
+            if (!ok) break;
+#pragma unroll
+            for (int c = P_STEPS; c < ROWS / 16; ++c)
+              if (c < steps) mma_f16_ts_by(leader, tm_o, tm_s + 8 * c, dv + 128 * c, id_o, 1u);
+            if (j == mine - 1) tc_commit_by(leader, b_o);
+          }
+          tc_commit_by(leader, empty_bar(sv));
+          if (more)
+            qk(j + 1, sk, true);
+          else if (leader)
+            mbar_arrive(turn_bar + 8 * (s ^ 1));
         }
-        kv += 2 * tiles;
       }
       // Every MMA issued completes before TMEM is released.
-      tc_commit_by(leader, final_bar);
-      drain_wait(final_bar, 0, 100000000ull);
+      tc_commit_by(leader, final_bar + 8 * s);
+      drain_wait(final_bar + 8 * s, 0, 100000000ull);
       __syncwarp();
     } else {
-      // --------------------------------------------------------- guards --
-      const int g = warp - GUARD_WARP;
+      // ---------------------------------------------------------- guard --
       uint32_t kv = 0, n = 0, phases = 0;
       bool ok = true;
       for (int64_t w = blockIdx.x; ok && items.get(p, w, it); w += gridDim.x, ++n) {
         const int tiles = max(it.tiles(0, p.causal), it.tiles(1, p.causal));
-        uint32_t* f = flags + 16 * (n & 1) + 8 * g;
+        uint32_t* f = flags + 8 * (n & 1);
         if (p.causal) {
           // the epilogues of the item before last have read these words
           if (n >= 2)
@@ -389,8 +426,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (lane < 8) f[lane] = 0u;
           __syncwarp();
         }
-        for (int j = 0; ok && j < tiles; ++j) {
-          if (!it.guarded(j, p.causal)) continue;
+        for (int j = it.guard_from(p.causal); ok && j < tiles; ++j) {
           const uint32_t u = kv + 2 * j + 1;
           const uint32_t st = u % STAGES;
           ok = __all_sync(0xFFFFFFFFu, svdq_wait(guard_go(st), (phases >> st) & 1u, SITE_GUARD_V) &&
@@ -398,31 +434,34 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (!ok) break;
           phases ^= 1u << st;
           const int valid = min(ROWS, it.len - j * ROWS);
-          const bool scan = p.causal && j >= it.q0 / ROWS;
-          uint32_t* fj = f + 4 * (j - it.q0 / ROWS);
+          uint32_t* fj = f + 4 * (j - it.q0 / ROWS);   // causal
+          // 16-byte words of the tile's boxes: eight per row
           const int stop = (valid + 15) / 16 * 16;
-          for (int c = 32 * g + lane; c < static_cast<int>(S_::TILE_BYTES / 16); c += 64) {
-            const int row = (c >> 3) & (ROWS - 1);
-            const uint32_t at = s_kv(st) + 16 * c;
-            if (row >= stop) continue;
-            if (row >= valid) {
-              st_shared_v4(at, 0u, 0u, 0u, 0u);
-            } else if (scan) {
-              uint32_t x[4];
-              ld_shared_v4(at, x[0], x[1], x[2], x[3]);
-              constexpr uint32_t m = BF16 ? 0x7F807F80u : 0x7C007C00u;
-              constexpr uint32_t one = BF16 ? 0x00800080u : 0x04000400u;
-              uint32_t bad = 0;
+          const uint32_t tile = s_kv(st);
+          for (int b = 0; b < NB; ++b)
+            for (int c = 8 * valid + lane; c < 8 * stop; c += 32)
+              st_shared_v4(tile + b * BOX_BYTES + 16 * c, 0u, 0u, 0u, 0u);
+          if (p.causal) {
+            for (int b = 0; b < NB; ++b) {
+#pragma unroll 8
+              for (int c = lane; c < 8 * valid; c += 32) {
+                const uint32_t at = tile + b * BOX_BYTES + 16 * c;
+                uint32_t x[4];
+                ld_shared_v4(at, x[0], x[1], x[2], x[3]);
+                constexpr uint32_t m = BF16 ? 0x7F807F80u : 0x7C007C00u;
+                constexpr uint32_t one = BF16 ? 0x00800080u : 0x04000400u;
+                uint32_t bad = 0;
 #pragma unroll
-              for (int i = 0; i < 4; ++i) bad |= ((x[i] & m) + one) & 0x80008000u;
-              if (bad != 0u) {
+                for (int i = 0; i < 4; ++i) bad |= (x[i] & m) + one;
+                if ((bad & 0x80008000u) != 0u) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  if (is_nonfinite16<BF16>(x[i])) x[i] &= 0xFFFF0000u;
-                  if (is_nonfinite16<BF16>(x[i] >> 16)) x[i] &= 0x0000FFFFu;
+                  for (int i = 0; i < 4; ++i) {
+                    if (is_nonfinite16<BF16>(x[i])) x[i] &= 0xFFFF0000u;
+                    if (is_nonfinite16<BF16>(x[i] >> 16)) x[i] &= 0x0000FFFFu;
+                  }
+                  st_shared_v4(at, x[0], x[1], x[2], x[3]);
+                  atomicOr(fj + (c >> 8), 1u << ((c >> 3) & 31));
                 }
-                st_shared_v4(at, x[0], x[1], x[2], x[3]);
-                atomicOr(fj + (row >> 5), 1u << (row & 31));
               }
             }
           }
@@ -450,7 +489,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const int row = it.q0 + slot * ROWS + r;   // of the sequence
       if (tiles > 0) {
         float m = -INFINITY;     // reference of the row, raw units of S
-        float l0 = 0.f, l1 = 0.f;
+        float off = 0.f;         // -m in log2 units
+        bool big = false;        // off is too large for one fma
+        uint64_t sum2 = 0;       // of the weights, even and odd keys
         for (int j = 0; j < tiles; ++j) {
           ok = __all_sync(0xFFFFFFFFu, svdq_wait(s_full(slot), ns++ & 1u, SITE_SOFT_S));
           if (!ok) break;
@@ -468,6 +509,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               for (int e = 0; e < 32; ++e)
                 if (32 * c + e >= keys) x[c][e] = 0xFF800000u;   // -inf
           }
+          // Weights 2^(x sc + off) of 32 keys, packed, and their sum.
+          auto weights = [&](const uint32_t (&xc)[32], uint32_t (&w16)[16], auto early) {
+            const uint64_t sc2 = pk(sc, sc), off2 = pk(off, off);
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              float a, b;
+              upk(fma2(pk(__uint_as_float(xc[2 * e]), __uint_as_float(xc[2 * e + 1])), sc2, off2), a, b);
+              a = decltype(early)::value ? ex2_here(a) : ex2_approx_ftz(a);
+              b = decltype(early)::value ? ex2_here(b) : ex2_approx_ftz(b);
+              sum[e & 1] = add2(sum[e & 1], pk(a, b));
+              w16[e] = pack2<BF16>(a, b);
+            }
+            return add2(sum[0], sum[1]);
+          };
+          // The first weights are taken with the present reference, beside
+          // the maximum that says whether it still holds: it nearly always
+          // does, so the maximum is off the way from S to P.
+          uint32_t w16[16];
+          uint64_t part = weights(x[0], w16, Tag<true>());
           float t[4] = {m, m, m, m};
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -475,50 +536,46 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int e = 0; e < 32; e += 2)
               t[(e >> 1) & 3] = max3(t[(e >> 1) & 3], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
           const float top = fmaxf(max3(t[0], t[1], t[2]), t[3]);
-          if (j == 0) {
-            m = top;
-          } else if (__any_sync(0xFFFFFFFFu, (top - m) * sc > RESCALE_LOG2)) {
-            // O is idle here: the commit behind s_full also covers this
-            // slot's previous P V.
-            const float f = top == m ? 1.f : ex2_approx_ftz((m - top) * sc);
-            m = top;
-            l0 *= f;
-            l1 *= f;
-            for (int c = 0; c < p.D; c += 16) {
-              uint32_t o[16];
-              tmem_ld_32x32b_x16(tm_o + c, o);
-              tmem_ld_wait();
+          const bool grown = __any_sync(0xFFFFFFFFu, (top - m) * sc > RESCALE_LOG2);
+          if (grown || big) {
+            if (grown) {
+              const float f = top == m ? 1.f : ex2_approx_ftz((m - top) * sc);
+              m = top;
+              sum2 = mul2(sum2, pk(f, f));
+              if (j > 0) {
+                // O is idle here: the commit behind s_full also covers this
+                // slot's previous P V.
+                for (int c = 0; c < p.D; c += 16) {
+                  uint32_t o[16];
+                  tmem_ld_32x32b_x16(tm_o + c, o);
+                  tmem_ld_wait();
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-              tmem_st_32x32b_x16(tm_o + c, o);
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st_32x32b_x16(tm_o + c, o);
+                }
+              }
+              off = m == -INFINITY ? 0.f : -m * sc;
+              big = __any_sync(0xFFFFFFFFu, fabsf(off) > 4096.f);
             }
-          }
-          // Exponents x sc - m sc in one fma: the rounding of m sc, 2^-24 of
-          // it, adds to the one S has anyway.  Where m sc is so large that
-          // this would show (2^-12 and more), m is taken off first.
-          float off = m == -INFINITY ? 0.f : -m * sc;
-          if (__any_sync(0xFFFFFFFFu, fabsf(off) > 4096.f)) {
-            const float ref = m == -INFINITY ? 0.f : m;
-            off = 0.f;
+            // Exponents x sc - m sc come from one fma: the rounding of m sc,
+            // 2^-24 of it, adds to the one S has anyway.  Where m sc is so
+            // large that this would show (2^-12 and more), m is taken off
+            // first.
+            if (big) {
+              const float ref = m == -INFINITY ? 0.f : m;
+              off = 0.f;
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
+              for (int c = 0; c < 4; ++c)
 #pragma unroll
-              for (int e = 0; e < 32; ++e) x[c][e] = __float_as_uint(__uint_as_float(x[c][e]) - ref);
-          }
-          const uint64_t sc2 = pk(sc, sc), off2 = pk(off, off);
-          uint64_t sum2 = pk(l0, l1);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w16[16];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              float a, b;
-              upk(fma2(pk(__uint_as_float(x[c][2 * e]), __uint_as_float(x[c][2 * e + 1])), sc2, off2), a, b);
-              a = ex2_approx_ftz(a);
-              b = ex2_approx_ftz(b);
-              sum2 = add2(sum2, pk(a, b));
-              w16[e] = pack2<BF16>(a, b);
+                for (int e = 0; e < 32; ++e) x[c][e] = __float_as_uint(__uint_as_float(x[c][e]) - ref);
             }
+            part = weights(x[0], w16, Tag<false>());
+          }
+          sum2 = add2(sum2, part);
+          tmem_st_32x32b_x16(tm_s, w16);
+#pragma unroll
+          for (int c = 1; c < 4; ++c) {
+            sum2 = add2(sum2, weights(x[c], w16, Tag<false>()));
             tmem_st_32x32b_x16(tm_s + 16 * c, w16);
             if (c >= 2) {   // P_STEPS steps of 16 keys are there, then the rest
               tmem_st_wait();
@@ -527,21 +584,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               if (lane == 0) mbar_arrive(c == 2 ? p_full(slot) : p_rest(slot));
             }
           }
-          upk(sum2, l0, l1);
         }
         if (!ok) break;
         // -------------------------------------------------------- epilogue --
         ok = __all_sync(0xFFFFFFFFu, svdq_wait(o_full(slot), no++ & 1u, SITE_SOFT_O));
         if (!ok) break;
         tc_fence_after();
+        float l0, l1;
+        upk(sum2, l0, l1);
         const float inv = 1.f / (l0 + l1);
-        const uint32_t* f = flags + 16 * (n & 1);
+        const uint32_t* f = flags + 8 * (n & 1);
         uint32_t noted = 0;
         if (p.causal) {
           ok = __all_sync(0xFFFFFFFFu, svdq_wait(flags_full(n & 1), (n >> 1) & 1u, SITE_SOFT_FLAGS));
           if (!ok) break;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) noted |= f[i];
+          for (int i = 0; i < 8; ++i) noted |= f[i];
         }
         uint16_t* dst = p.out + static_cast<int64_t>(it.begin + row) * p.ost + it.head * p.osh;
         for (int c = 0; c < p.D; c += 16) {
@@ -554,7 +612,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (noted != 0u) {
             // Non-finite values of the diagonal tiles: into the rows that attend them.
             for (int i = 0; i < 8; ++i) {
-              for (uint32_t b = f[i] | f[i + 8]; b != 0u; b &= b - 1) {
+              for (uint32_t b = f[i]; b != 0u; b &= b - 1) {
                 const int key = it.q0 + 32 * i + __ffs(b) - 1;
                 if (key > row) continue;
                 const uint16_t* src = p.v + static_cast<int64_t>(it.begin + key) * p.vst +

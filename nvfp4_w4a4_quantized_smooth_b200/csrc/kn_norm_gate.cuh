@@ -94,6 +94,12 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
   return v;
 }
 
+// A truth value as an argument's type.
+template <bool B>
+struct Tag {
+  static constexpr bool value = B;
+};
+
 namespace kn {
 
 constexpr int MAX_THREADS = 512;

@@ -37,11 +37,6 @@ constexpr uint32_t UNIT_BYTES = 4096;       // heads of one token that a unit ta
 constexpr uint32_t SMEM_BYTES = WARPS * RING * UNIT_BYTES;
 constexpr uint32_t SITE_UNIT = 0x68;
 
-template <bool B>
-struct Tag {
-  static constexpr bool value = B;
-};
-
 struct Params {
   const uint16_t *q, *k, *qw, *kw;
   uint16_t *qo, *ko;
