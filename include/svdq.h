@@ -303,8 +303,8 @@ int svdq_quantize_weights_noalloc(const uint16_t* W, const uint16_t* smooth, con
  * - Strides are in elements, multiples of 8; 16-bit tensors are 16-byte
  *   aligned.  The stride of a dimension of size one is not used.
  * - T = 0 returns SVDQ_OK and enqueues nothing.
- * - No workspace: calls on several streams, and captured calls, share
- *   nothing but their own tensors.
+ * - The library keeps nothing between calls: calls on several streams, and
+ *   captured calls, share nothing but the memory they are given.
  * - Outputs that meet inputs in memory give SVDQ_ERR_INVALID_ARG, unless a
  *   call says otherwise.  (Decided from the addresses and strides: operands
  *   side by side in the rows of one buffer are recognised as apart; two
@@ -383,13 +383,25 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
  * a row does not attend, whatever they hold (inf, NaN), do not reach it.
  *   q [T, Hq, D], k, v [T, Hk, D], out [T, Hq, D]  by strides (token, head).
  *   scale         finite and positive (usually 1 / sqrt(D)).
+ *   workspace     NULL, or svdq_attention_workspace_bytes(T, Hq, D) bytes
+ *                 (which depends on the device; 0: none is of use), 16-byte
+ *                 aligned, overwritten.  With it, where rows are too few to
+ *                 fill the device evenly, the key tiles are divided among
+ *                 the SMs and the parts joined by a second kernel, in a
+ *                 fixed order.  Results repeat bit for bit for the same call
+ *                 on the same device; with and without workspace they may
+ *                 differ in the last bits of the fp32 sums.  Calls that may
+ *                 overlap on the GPU need workspaces of their own.
  * Limits: Hq % Hk == 0, D % 8 == 0, D <= 128 (else SVDQ_ERR_SHAPE /
  * SVDQ_ERR_UNSUPPORTED). */
+size_t svdq_attention_workspace_bytes(int T, int Hq, int D);
+
 int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h,
                    const uint16_t* k, int64_t k_stride_t, int64_t k_stride_h, const uint16_t* v,
                    int64_t v_stride_t, int64_t v_stride_h, int T, int Hq, int Hk, int D,
                    const int32_t* cu_seqlens, int n_seqs, int causal, float scale, uint16_t* out,
-                   int64_t o_stride_t, int64_t o_stride_h, void* stream);
+                   int64_t o_stride_t, int64_t o_stride_h, void* workspace,
+                   size_t workspace_bytes, void* stream);
 
 /* ---- helpers ------------------------------------------------------------ */
 

@@ -52,6 +52,7 @@ constexpr uint32_t BOX_BYTES = ROWS * 128;   // 128 rows x 64 elements, 128-byte
 constexpr uint32_t TMEM_COLS = 512;
 constexpr uint32_t TM_S = 0;            // S / P of slot s at 128 s
 constexpr uint32_t TM_O = 256;          // O of slot s at 256 + 128 s
+constexpr int MIN_RUN = 4;               // key tiles of a block's run, at least (split)
 constexpr int P_STEPS = 6;              // 16-key steps of P that are handed over first
 constexpr float RESCALE_LOG2 = 8.f;
 // Registers per thread of the softmax warps and of the others.
@@ -82,6 +83,25 @@ constexpr uint32_t SITE_TMA_Q = 0x50, SITE_TMA_KV = 0x51, SITE_MMA_Q = 0x52, SIT
                    SITE_SOFT_O = 0x57, SITE_GUARD_V = 0x58, SITE_GUARD_FLAGS = 0x59,
                    SITE_SOFT_FLAGS = 0x5A, SITE_MMA_TURN = 0x5B;
 
+// What a block leaves of an item that it has only some key tiles of: a row's
+// reference, sum and unscaled O in the workspace, and this.
+struct Meta {
+  int valid, last;          // last: up to the item's last key tile
+  int begin, len, q0, head;
+  int pad[2];
+};
+
+// Workspace of a launch of `blocks`: two partial results per block (an item
+// begun by the block in front, an item left to the one behind).
+struct Workspace {
+  float* o;                 // [2 blocks][256][dp]
+  float2* ml;               // [2 blocks][256]  reference, sum
+  Meta* meta;               // [2 blocks]
+  static constexpr size_t bytes(int blocks, int dp) {
+    return static_cast<size_t>(2) * blocks * (ITEM_ROWS * (4u * dp + 8u) + sizeof(Meta));
+  }
+};
+
 struct Params {
   const int32_t* cu;        // [S + 1] or NULL: one sequence of all T rows
   const uint16_t* v;        // for the non-finite values' way back
@@ -90,33 +110,57 @@ struct Params {
   int T, S, Hq, group, D;
   int causal;
   float scale_log2;         // scale * log2(e)
+  int split;                // items divided among the blocks
+  Workspace ws;             // split
 };
 
-// One work item: rows [q0, q0 + 256) of the sequence [begin, begin + len), head h.
+// One work item: rows [q0, q0 + 256) of the sequence [begin, begin + len),
+// head h, and of its key tiles the range [ka, kb).
 struct Item {
-  int begin, len, q0, head;
+  int begin, len, q0, head, ka, kb;
   __device__ __forceinline__ int key_tiles() const { return (len + ROWS - 1) / ROWS; }
-  // key tiles that slot s reads
+  // key tiles of slot s: it attends [0, tiles), and reads [ka, end) of them
   __device__ __forceinline__ int tiles(int s, int causal) const {
     if (q0 + s * ROWS >= len) return 0;
     const int n = key_tiles();
     return causal ? min(n, q0 / ROWS + s + 1) : n;
   }
+  __device__ __forceinline__ int all_tiles(int causal) const {
+    return max(tiles(0, causal), tiles(1, causal));
+  }
+  __device__ __forceinline__ int end(int s, int causal) const { return min(kb, tiles(s, causal)); }
+  __device__ __forceinline__ bool whole(int causal) const { return ka == 0 && kb == all_tiles(causal); }
   // The first guarded value tile: the diagonal's (and all behind it), or the
   // last one where it ends inside 16 keys.
   __device__ __forceinline__ int guard_from(int causal) const {
-    return causal ? q0 / ROWS : len % 16 != 0 ? key_tiles() - 1 : INT_MAX;
+    return max(ka, causal ? q0 / ROWS : len % 16 != 0 ? key_tiles() - 1 : INT_MAX);
   }
 };
 
-// Walks the work items of all sequences in order.  Every warp runs its own
-// copy; w must not decrease from call to call.  Offsets are clamped to
+// Walks a block's work.  Every warp runs its own copy.  Offsets are clamped to
 // [0, T] and to an increasing order, so that no entry of cu can lead outside
 // the tensors.
+//
+// Whole items: block b takes the items b, b + blocks, ... of all sequences
+// (causal: longest first within a sequence).  Split: the key tiles of all
+// items in one line are cut into equal runs, one per block, so that no SM
+// waits for another's last item and a few long rows still fill the device.
 struct Items {
-  int s0 = 0;        // first sequence of the present group of 32
-  int64_t base = 0;  // items in front of it
-  __device__ __forceinline__ bool get(const Params& p, int64_t w, Item& it) {
+  int s0 = 0;             // first sequence of the present group of 32
+  int64_t base = 0;       // items (split: key tiles) in front of it
+  int64_t at = 0, end = 0;
+
+  // Of a sequence: items, or key tiles of one head's items.
+  static __device__ __forceinline__ int64_t size(const Params& p, int len) {
+    const int64_t nt = (len + ITEM_ROWS - 1) / ITEM_ROWS;
+    if (!p.split) return nt * p.Hq;
+    const int64_t nk = (len + ROWS - 1) / ROWS;
+    // causal: 2, 4, 6, ... tiles, the last item one fewer where it has one slot
+    return (p.causal ? nt * (nt + 1) - (2 * nt - nk) : nt * nk) * p.Hq;
+  }
+  // The sequence that holds place w (which must not fall from call to call).
+  // Returns the place within the sequence, -1 behind the last.
+  __device__ __forceinline__ int64_t find(const Params& p, int64_t w, int& begin_out, int& len_out) {
     const int lane = threadIdx.x & 31;
     while (s0 < p.S) {
       const int s = s0 + lane;
@@ -125,7 +169,7 @@ struct Items {
         begin = p.cu ? min(max(p.cu[s], 0), p.T) : 0;
         len = (p.cu ? min(max(p.cu[s + 1], begin), p.T) : p.T) - begin;
       }
-      const int64_t n = static_cast<int64_t>((len + ITEM_ROWS - 1) / ITEM_ROWS) * p.Hq;
+      const int64_t n = size(p, len);
       int64_t incl = n;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -135,23 +179,83 @@ struct Items {
       const uint32_t mine = __ballot_sync(0xFFFFFFFFu, base + incl > w);
       if (mine != 0u) {
         const int src = __ffs(mine) - 1;
-        const int r = static_cast<int>(__shfl_sync(0xFFFFFFFFu, w - base - (incl - n), src));
-        it.begin = __shfl_sync(0xFFFFFFFFu, begin, src);
-        it.len = __shfl_sync(0xFFFFFFFFu, len, src);
-        const int nt = (it.len + ITEM_ROWS - 1) / ITEM_ROWS;
-        if (p.causal) {   // longest items first
-          it.head = r % p.Hq;
-          it.q0 = (nt - 1 - r / p.Hq) * ITEM_ROWS;
-        } else {          // the items of one head together: they read the same keys
-          it.head = r / nt;
-          it.q0 = (r % nt) * ITEM_ROWS;
-        }
-        return true;
+        begin_out = __shfl_sync(0xFFFFFFFFu, begin, src);
+        len_out = __shfl_sync(0xFFFFFFFFu, len, src);
+        return __shfl_sync(0xFFFFFFFFu, w - base - (incl - n), src);
       }
       base += __shfl_sync(0xFFFFFFFFu, incl, 31);
       s0 += 32;
     }
-    return false;
+    return -1;
+  }
+  // Split: the item at place w of the line of key tiles, and the place in it.
+  __device__ __forceinline__ bool locate(const Params& p, int64_t w, Item& it) {
+    const int64_t r = find(p, w, it.begin, it.len);
+    if (r < 0) return false;
+    const int64_t per = size(p, it.len) / p.Hq;
+    it.head = static_cast<int>(r / per);
+    const int64_t r2 = r - it.head * per;
+    if (p.causal) {
+      // i (i + 1) tiles in front of item i
+      int64_t i = static_cast<int64_t>((sqrtf(4.f * static_cast<float>(r2) + 1.f) - 1.f) * 0.5f);
+      while (i > 0 && i * (i + 1) > r2) --i;
+      while ((i + 1) * (i + 2) <= r2) ++i;
+      it.q0 = static_cast<int>(i) * ITEM_ROWS;
+      it.ka = static_cast<int>(r2 - i * (i + 1));
+    } else {
+      const int nk = it.key_tiles();
+      it.q0 = static_cast<int>(r2 / nk) * ITEM_ROWS;
+      it.ka = static_cast<int>(r2 % nk);
+    }
+    return true;
+  }
+  // Where block b's run begins: the equal share, moved to an item's edge where
+  // one is near (two partial results less).
+  static __device__ __forceinline__ int64_t edge(const Params& p, int64_t w, int64_t total, int64_t run) {
+    if (w >= total) return total;
+    Items f;
+    Item it;
+    f.locate(p, w, it);
+    const int n = it.all_tiles(p.causal);
+    const int64_t near = max(static_cast<int64_t>(1), run / 16);
+    if (it.ka <= near) return w - it.ka;
+    if (n - it.ka <= near) return w + n - it.ka;
+    return w;
+  }
+  __device__ __forceinline__ void start(const Params& p) {
+    at = blockIdx.x;
+    if (!p.split) return;
+    int b, l;
+    Items all;
+    all.find(p, INT64_MAX, b, l);
+    const int64_t total = all.base;
+    const int64_t run = max(static_cast<int64_t>(MIN_RUN), (total + gridDim.x - 1) / gridDim.x);
+    at = edge(p, blockIdx.x * run, total, run);
+    end = edge(p, (blockIdx.x + 1) * run, total, run);
+  }
+  __device__ __forceinline__ bool get(const Params& p, Item& it) {
+    if (p.split) {
+      if (at >= end || !locate(p, at, it)) return false;
+      const int64_t left = end - at;
+      const int n = it.all_tiles(p.causal);
+      it.kb = n - it.ka <= left ? n : it.ka + static_cast<int>(left);
+      at += it.kb - it.ka;
+      return true;
+    }
+    const int r = static_cast<int>(find(p, at, it.begin, it.len));
+    if (r < 0) return false;
+    at += gridDim.x;
+    const int nt = (it.len + ITEM_ROWS - 1) / ITEM_ROWS;
+    if (p.causal) {   // longest items first
+      it.head = r % p.Hq;
+      it.q0 = (nt - 1 - r / p.Hq) * ITEM_ROWS;
+    } else {          // the items of one head together: they read the same keys
+      it.head = r / nt;
+      it.q0 = (r % nt) * ITEM_ROWS;
+    }
+    it.ka = 0;
+    it.kb = it.all_tiles(p.causal);
+    return true;
   }
 };
 
@@ -256,27 +360,26 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 
   Items items;
   Item it;
+  items.start(p);
   if (warp >= MMA_WARP) {
     set_max_regs_down<OTHER_REGS>();
     if (warp == TMA_WARP) {
       // ------------------------------------------------------------ TMA --
       uint32_t kv = 0, n = 0;   // ring uses, items
       bool ok = true;
-      for (int64_t w = blockIdx.x; ok && items.get(p, w, it); w += gridDim.x, ++n) {
+      for (; ok && items.get(p, it); ++n) {
         if (lane == 0) {
-          const int n0 = it.tiles(0, p.causal), n1 = it.tiles(1, p.causal);
-          const int tiles = max(n0, n1);
           const int kh = it.head / p.group;
           ok = svdq_wait(q_empty, (n & 1u) ^ 1u, SITE_TMA_Q);
           if (ok) {
-            const int slots = n1 > 0 ? 2 : 1;
+            const int slots = it.q0 + ROWS < it.len ? 2 : 1;
             mbar_arrive_expect_tx(q_full, slots * S_::TILE_BYTES);
             for (int s = 0; s < slots; ++s)
               for (int b = 0; b < NB; ++b)
                 tma_load_3d(s_q(s) + b * BOX_BYTES, &tm_q, 64 * b, it.head,
                             it.begin + it.q0 + s * ROWS, q_full);
           }
-          for (int j = 0; ok && j < 2 * tiles; ++j, ++kv) {
+          for (int j = 2 * it.ka; ok && j < 2 * it.kb; ++j, ++kv) {
             const uint32_t st = kv % STAGES;
             ok = svdq_wait(empty_bar(st), ((kv / STAGES) & 1u) ^ 1u, SITE_TMA_KV);
             if (!ok) break;
@@ -330,9 +433,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto next = [&]() {
         if (++st == STAGES) st = 0, ph ^= 1u;
       };
-      for (int64_t w = blockIdx.x; ok && items.get(p, w, it); w += gridDim.x, ++n) {
-        const int mine = it.tiles(s, p.causal);            // key tiles of this slot
-        const int tiles = max(it.tiles(0, p.causal), it.tiles(1, p.causal));
+      for (; ok && items.get(p, it); ++n) {
+        const int mine = it.end(s, p.causal);   // where this slot's key tiles end
         const int last = it.key_tiles() - 1;
         const int last_steps = (it.len - last * ROWS + 15) / 16;   // 16-key steps of the last tile
         const int guard_from = it.guard_from(p.causal);
@@ -354,19 +456,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mbar_arrive(turn_bar + 8 * (s ^ 1));
           }
           tc_commit_by(leader, empty_bar(at));
-          if (j == tiles - 1) tc_commit_by(leader, q_empty);
+          if (j == it.kb - 1) tc_commit_by(leader, q_empty);
         };
         wait(q_full, n & 1u, SITE_MMA_Q);
         wait(full_bar(st), ph, SITE_MMA_KV);
         tc_fence_after();
         if (!ok) break;
-        qk(0, st, false);
+        qk(it.ka, st, false);
         next();
-        for (int j = 0; j < tiles; ++j) {
+        for (int j = it.ka; j < it.kb; ++j) {
           // All that the turn's products need is there before it is taken.
           const uint32_t sv = st;
           const uint64_t dv = desc_v + TILE_16 * sv;
-          const bool more = j + 1 < tiles;
+          const bool more = j + 1 < it.kb;
           wait(full_bar(sv), ph, SITE_MMA_KV);
           if (j >= guard_from) {
             wait(guard_done(sv), (guards >> sv) & 1u, SITE_MMA_GUARD);
@@ -390,7 +492,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
             for (int c = 0; c < P_STEPS; ++c)
               if (c < steps)
-                mma_f16_ts_by(leader, tm_o, tm_s + 8 * c, dv + 128 * c, id_o, c == 0 ? j != 0 : 1u);
+                mma_f16_ts_by(leader, tm_o, tm_s + 8 * c, dv + 128 * c, id_o, c == 0 ? j != it.ka : 1u);
             wait(b_rest, np++ & 1u, SITE_MMA_P);
             tc_fence_after();
             if (!ok) break;
@@ -413,9 +515,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else {
       // ---------------------------------------------------------- guard --
       uint32_t kv = 0, n = 0, phases = 0;
+      Meta meta[2] = {};   // split: this block's partial results
       bool ok = true;
-      for (int64_t w = blockIdx.x; ok && items.get(p, w, it); w += gridDim.x, ++n) {
-        const int tiles = max(it.tiles(0, p.causal), it.tiles(1, p.causal));
+      for (; ok && items.get(p, it); ++n) {
         uint32_t* f = flags + 8 * (n & 1);
         if (p.causal) {
           // the epilogues of the item before last have read these words
@@ -426,8 +528,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (lane < 8) f[lane] = 0u;
           __syncwarp();
         }
-        for (int j = it.guard_from(p.causal); ok && j < tiles; ++j) {
-          const uint32_t u = kv + 2 * j + 1;
+        for (int j = it.guard_from(p.causal); ok && j < it.kb; ++j) {
+          const uint32_t u = kv + 2 * (j - it.ka) + 1;
           const uint32_t st = u % STAGES;
           ok = __all_sync(0xFFFFFFFFu, svdq_wait(guard_go(st), (phases >> st) & 1u, SITE_GUARD_V) &&
                                            svdq_wait(full_bar(st), (u / STAGES) & 1u, SITE_GUARD_V));
@@ -470,7 +572,17 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           if (lane == 0) mbar_arrive(guard_done(st));
         }
         if (ok && p.causal && lane == 0) mbar_arrive(flags_full(n & 1));
-        kv += 2 * tiles;
+        kv += 2 * (it.kb - it.ka);
+        if (p.split && lane == 0 && !it.whole(p.causal)) {
+          Meta& m = meta[it.ka > 0 ? 0 : 1];
+          m.valid = 1;
+          m.last = it.kb == it.all_tiles(p.causal);
+          m.begin = it.begin, m.len = it.len, m.q0 = it.q0, m.head = it.head;
+        }
+      }
+      if (p.split && lane == 0) {
+        p.ws.meta[2 * blockIdx.x] = meta[0];
+        p.ws.meta[2 * blockIdx.x + 1] = meta[1];
       }
     }
   } else {
@@ -484,15 +596,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const float sc = p.scale_log2;
     uint32_t ns = 0, no = 0, n = 0;         // S tiles, O tiles waited for, items
     bool ok = true;
-    for (int64_t w = blockIdx.x; ok && items.get(p, w, it); w += gridDim.x, ++n) {
-      const int tiles = it.tiles(slot, p.causal);
+    for (; ok && items.get(p, it); ++n) {
+      const int stop = it.end(slot, p.causal);   // its key tiles here are [ka, stop)
+      const bool whole = it.whole(p.causal);
+      auto notes = [&]() {   // the guard has been through this item
+        return __all_sync(0xFFFFFFFFu, svdq_wait(flags_full(n & 1), (n >> 1) & 1u, SITE_SOFT_FLAGS)) != 0;
+      };
       const int row = it.q0 + slot * ROWS + r;   // of the sequence
-      if (tiles > 0) {
+      if (stop > it.ka) {
         float m = -INFINITY;     // reference of the row, raw units of S
         float off = 0.f;         // -m in log2 units
         bool big = false;        // off is too large for one fma
         uint64_t sum2 = 0;       // of the weights, even and odd keys
-        for (int j = 0; j < tiles; ++j) {
+        for (int j = it.ka; j < stop; ++j) {
           ok = __all_sync(0xFFFFFFFFu, svdq_wait(s_full(slot), ns++ & 1u, SITE_SOFT_S));
           if (!ok) break;
           tc_fence_after();
@@ -542,7 +658,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               const float f = top == m ? 1.f : ex2_approx_ftz((m - top) * sc);
               m = top;
               sum2 = mul2(sum2, pk(f, f));
-              if (j > 0) {
+              if (j > it.ka) {
                 // O is idle here: the commit behind s_full also covers this
                 // slot's previous P V.
                 for (int c = 0; c < p.D; c += 16) {
@@ -592,16 +708,20 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         tc_fence_after();
         float l0, l1;
         upk(sum2, l0, l1);
-        const float inv = 1.f / (l0 + l1);
+        // A partial result stays unscaled, in fp32.
+        const float inv = whole ? 1.f / (l0 + l1) : 1.f;
         const uint32_t* f = flags + 8 * (n & 1);
         uint32_t noted = 0;
         if (p.causal) {
-          ok = __all_sync(0xFFFFFFFFu, svdq_wait(flags_full(n & 1), (n >> 1) & 1u, SITE_SOFT_FLAGS));
+          ok = notes();
           if (!ok) break;
 #pragma unroll
           for (int i = 0; i < 8; ++i) noted |= f[i];
         }
         uint16_t* dst = p.out + static_cast<int64_t>(it.begin + row) * p.ost + it.head * p.osh;
+        const int prow = (2 * blockIdx.x + (it.ka > 0 ? 0 : 1)) * ITEM_ROWS + slot * ROWS + r;
+        float* part = p.ws.o + static_cast<size_t>(prow) * ((p.D + 15) / 16 * 16);
+        if (!whole) p.ws.ml[prow] = make_float2(m, l0 + l1);
         for (int c = 0; c < p.D; c += 16) {
           uint32_t o[16];
           tmem_ld_32x32b_x16(tm_o + c, o);
@@ -628,7 +748,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               }
             }
           }
-          if (row < it.len) {
+          if (!whole) {
+            float4* o4 = reinterpret_cast<float4*>(part + c);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o4[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+          } else if (row < it.len) {
             const float (&a)[8] = reinterpret_cast<const float (&)[8]>(v[0]);
             const float (&b)[8] = reinterpret_cast<const float (&)[8]>(v[8]);
             *reinterpret_cast<uint4*>(dst + c) = pack8<BF16>(a);
@@ -636,8 +760,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           }
         }
         tc_fence_before();
+      } else if (!whole && it.q0 + slot * ROWS < it.len) {
+        // (causal, the item's last key tile alone: nothing for slot 0)
+        p.ws.ml[(2 * blockIdx.x + (it.ka > 0 ? 0 : 1)) * ITEM_ROWS + slot * ROWS + r] =
+            make_float2(-INFINITY, 0.f);
       }
       if (p.causal) {
+        // (also a slot that had nothing here waits for the notes: else it
+        // would run ahead and arrive for a later item in this one's phase)
+        if (stop <= it.ka) ok = notes();
         __syncwarp();
         if (lane == 0) mbar_arrive(flags_free(n & 1));
       }
@@ -652,6 +783,67 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem, TMEM_COLS);
+  }
+}
+
+// Joins the partial results of split items.  An item begins in block b's
+// second one and goes on in the first ones of the blocks behind b, up to the
+// one that has its last key tile: the rows' references are brought to the
+// largest, sums and O added in that order, O divided by the sum.  Grid
+// (blocks, JOIN_PARTS): each block 256 / JOIN_PARTS rows, a warp per row.
+constexpr int JOIN_PARTS = 8;
+constexpr int JOIN_THREADS = 256;
+
+template <bool BF16>
+__global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Params p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int b = blockIdx.x, blocks = gridDim.x;
+  const Meta first = p.ws.meta[2 * b + 1];
+  if (!first.valid) return;
+  int parts = 1;
+  for (bool last = first.last; !last && b + parts < blocks; ++parts) {
+    const Meta& m = p.ws.meta[2 * (b + parts)];
+    if (!m.valid) break;
+    last = m.last;
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int dp = (p.D + 15) / 16 * 16;
+  const int col = 4 * lane;
+  constexpr int ROWS_EACH = ITEM_ROWS / JOIN_PARTS;
+  for (int i = warp; i < ROWS_EACH; i += JOIN_THREADS / 32) {
+    const int r = blockIdx.y * ROWS_EACH + i;
+    const int row = first.q0 + r;
+    if (row >= first.len) break;
+    auto place = [&](int k) {
+      return static_cast<size_t>(k == 0 ? 2 * b + 1 : 2 * (b + k)) * ITEM_ROWS + r;
+    };
+    float top = -INFINITY;
+    for (int k = lane; k < parts; k += 32) top = fmaxf(top, p.ws.ml[place(k)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+      const float2 ml = p.ws.ml[place(k)];
+      const float f = ml.x == top ? 1.f : ex2_approx_ftz((ml.x - top) * p.scale_log2);
+      l = fmaf(ml.y, f, l);
+      // (a part without a key for the row has written no O)
+      if (ml.x != -INFINITY && col < dp) {
+        const float4 v = *reinterpret_cast<const float4*>(p.ws.o + place(k) * dp + col);
+        o.x = fmaf(v.x, f, o.x);
+        o.y = fmaf(v.y, f, o.y);
+        o.z = fmaf(v.z, f, o.z);
+        o.w = fmaf(v.w, f, o.w);
+      }
+    }
+    const float inv = 1.f / l;
+    if (col < p.D) {
+      uint16_t* dst = p.out + static_cast<int64_t>(first.begin + row) * p.ost + first.head * p.osh + col;
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
+    }
   }
 }
 

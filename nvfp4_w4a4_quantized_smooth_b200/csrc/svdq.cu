@@ -1133,6 +1133,15 @@ int block_setup(DeviceInfo* d) {
   return SVDQ_OK;
 }
 
+// Whether the attention divides work items among the blocks: where there are
+// fewer than eight whole items per SM (a last, partly filled round of items
+// then costs more than an eighth), and more key tiles than a block's least
+// run (else no item is ever cut).
+bool ka_may_split(DeviceInfo* d, int T, int Hq) {
+  const int64_t items = (static_cast<int64_t>(T) + svdq::ka::ITEM_ROWS - 1) / svdq::ka::ITEM_ROWS * Hq;
+  return T > svdq::ka::MIN_RUN * svdq::ka::ROWS && items < static_cast<int64_t>(8) * d->num_sms;
+}
+
 bool bad_norm(int kind) { return kind < 0 || kind > SVDQ_NORM_LAYER; }
 
 }  // namespace
@@ -1335,11 +1344,20 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
   return launch_status();
 }
 
+size_t svdq_attention_workspace_bytes(int T, int Hq, int D) {
+  if (T < 1 || Hq < 1 || D < 8 || D % 8 || D > svdq::ka::MAX_D) return 0;
+  DeviceInfo* d = nullptr;
+  if (device_setup(&d)) return 0;
+  if (!ka_may_split(d, T, Hq)) return 0;
+  return svdq::ka::Workspace::bytes(d->num_sms, (D + 15) / 16 * 16);
+}
+
 int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h,
                    const uint16_t* k, int64_t k_stride_t, int64_t k_stride_h, const uint16_t* v,
                    int64_t v_stride_t, int64_t v_stride_h, int T, int Hq, int Hk, int D,
                    const int32_t* cu_seqlens, int n_seqs, int causal, float scale, uint16_t* out,
-                   int64_t o_stride_t, int64_t o_stride_h, void* stream) {
+                   int64_t o_stride_t, int64_t o_stride_h, void* workspace,
+                   size_t workspace_bytes, void* stream) {
   if (dtype != SVDQ_BF16 && dtype != SVDQ_FP16) return SVDQ_ERR_INVALID_ARG;
   if (!std::isfinite(scale) || scale <= 0.f) return SVDQ_ERR_INVALID_ARG;
   if (T < 0 || Hq < 1 || Hk < 1 || Hq % Hk || D < 1 || n_seqs < 1 || (!cu_seqlens && n_seqs != 1))
@@ -1360,7 +1378,7 @@ int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_s
   };
   if (misaligned(q, q_stride_t, q_stride_h, Hq) || misaligned(k, k_stride_t, k_stride_h, Hk) ||
       misaligned(v, v_stride_t, v_stride_h, Hk) || misaligned(out, o_stride_t, o_stride_h, Hq) ||
-      !aligned(cu_seqlens, 4))
+      !aligned(cu_seqlens, 4) || !aligned(workspace, 16))
     return SVDQ_ERR_ALIGNMENT;
   // Strides of a dimension of one are not used.
   if (T == 1) q_stride_t = k_stride_t = v_stride_t = o_stride_t = D;
@@ -1374,6 +1392,12 @@ int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_s
   const Extent ev = extent(v, T, v_stride_t, Hk, v_stride_h, D);
   const Extent eo = extent(out, T, o_stride_t, Hq, o_stride_h, D);
   if (may_meet(eo, eq) || may_meet(eo, ek) || may_meet(eo, ev)) return SVDQ_ERR_INVALID_ARG;
+  if (workspace) {
+    const Extent ew = {reinterpret_cast<uintptr_t>(workspace), 1, 0, 1, 0,
+                       static_cast<int64_t>(workspace_bytes)};
+    for (const Extent& e : {eq, ek, ev, eo})
+      if (may_meet(ew, e)) return SVDQ_ERR_INVALID_ARG;
+  }
   DeviceInfo* d = nullptr;
   if (int st = device_setup(&d)) return st;
   if (int st = block_setup(d)) return st;
@@ -1391,9 +1415,21 @@ int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_s
   p.vst = v_stride_t, p.vsh = v_stride_h, p.ost = o_stride_t, p.osh = o_stride_h;
   p.T = T, p.S = n_seqs, p.Hq = Hq, p.group = Hq / Hk, p.D = D, p.causal = causal ? 1 : 0;
   p.scale_log2 = scale * 1.44269504088896341f;
-  // At most this many work items; one persistent block per SM takes them in turn.
+  // At most this many work items; one persistent block per SM takes them in
+  // turn, or an equal share of their key tiles.
   const int64_t items = (static_cast<int64_t>(T) / ka::ITEM_ROWS + n_seqs) * Hq;
-  const unsigned grid = static_cast<unsigned>(items < d->num_sms ? items : d->num_sms);
+  unsigned grid = static_cast<unsigned>(items < d->num_sms ? items : d->num_sms);
+  const int dp = (D + 15) / 16 * 16;
+  p.split = workspace && ka_may_split(d, T, Hq) ? 1 : 0;
+  p.ws = {};
+  if (p.split) {
+    grid = d->num_sms;
+    if (workspace_bytes < ka::Workspace::bytes(grid, dp)) return SVDQ_ERR_INVALID_ARG;
+    const size_t rows = static_cast<size_t>(2) * grid * ka::ITEM_ROWS;
+    p.ws.o = static_cast<float*>(workspace);
+    p.ws.ml = reinterpret_cast<float2*>(p.ws.o + rows * dp);
+    p.ws.meta = reinterpret_cast<ka::Meta*>(p.ws.ml + rows);
+  }
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   const bool wide = D > 64;
@@ -1406,6 +1442,13 @@ int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_s
           : (wide ? cudaLaunchKernelEx(&cfg, ka::attention_kernel<false, 2>, tm_q, tm_k, tm_v, p)
                   : cudaLaunchKernelEx(&cfg, ka::attention_kernel<false, 1>, tm_q, tm_k, tm_v, p));
   if (e != cudaSuccess) return SVDQ_ERR_CUDA;
+  if (p.split) {
+    pdl_config(&cfg, &attr, grid, ka::JOIN_THREADS, 0, stream);
+    cfg.gridDim.y = ka::JOIN_PARTS;
+    if ((dtype == SVDQ_BF16 ? cudaLaunchKernelEx(&cfg, ka::join_kernel<true>, p)
+                            : cudaLaunchKernelEx(&cfg, ka::join_kernel<false>, p)) != cudaSuccess)
+      return SVDQ_ERR_CUDA;
+  }
   return launch_status();
 }
 

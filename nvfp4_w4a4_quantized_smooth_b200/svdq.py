@@ -77,7 +77,8 @@ SIGNATURES = {
     "svdq_rope_qk": (_I, [_I, _P, _L, _L, _I, _P, _L, _L, _I, _I, _I, _P, _L, _P, _I, _P, _I, _P,
                           _P, _F, _P, _L, _L, _P, _L, _L, _P]),
     "svdq_attention": (_I, [_I, _P, _L, _L, _P, _L, _L, _P, _L, _L, _I, _I, _I, _I, _P, _I, _I,
-                            _F, _P, _L, _L, _P]),
+                            _F, _P, _L, _L, _P, _SZ, _P]),
+    "svdq_attention_workspace_bytes": (_SZ, [_I, _I, _I]),
     "svdq_check_device_error": (_I, [_P]),
     "svdq_set_wait_timeout_ns": (_I, [ctypes.c_uint64]),
     "svdq_wait_probe": (_I, [_I, _P]),
@@ -652,10 +653,14 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         if out is None:
             out = q.new_empty((T, Hq, D))
         os_ = _need_like(out, dtype, index, shape, "out")
+        ws, size = None, _lib.svdq_attention_workspace_bytes(T, Hq, D) if T > 512 else 0
+        if size:
+            ws = torch.empty(size, dtype=torch.uint8, device=q.device)
         _check(_lib.svdq_attention(
             code, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
             vs[1], T, Hq, Hk, D, None if cu_seqlens is None else cu_seqlens.data_ptr(), S,
-            1 if causal else 0, scale, out.data_ptr(), os_[0], os_[1], s),
+            1 if causal else 0, scale, out.data_ptr(), os_[0], os_[1],
+            None if ws is None else ws.data_ptr(), size, s),
             "svdq_attention")
     return out
 

@@ -144,7 +144,7 @@ def attn_args(**kw):
     # q | k | v in the rows of one buffer, out apart
     a = dict(dtype=0, q=1 * MB, qst=512, qsh=64, k=1 * MB + 512, kst=512, ksh=64, v=1 * MB + 768,
              vst=512, vsh=64, T=16, Hq=4, Hk=2, D=64, cu=None, S=1, causal=0, scale=0.125, out=3 * MB,
-             ost=256, osh=64, stream=None)
+             ost=256, osh=64, ws=None, ws_bytes=0, stream=None)
     a.update(kw)
     return list(a.values())
 
@@ -162,7 +162,8 @@ ATTN_BAD = [
     ("UNSUPPORTED", dict(Hq=1 << 20, Hk=1 << 20, T=1 << 20)),
     ("UNSUPPORTED", dict(qst=1 << 39)),
     ("ALIGNMENT", dict(k=MB + 520)), ("ALIGNMENT", dict(vst=516)), ("ALIGNMENT", dict(osh=68)),
-    ("ALIGNMENT", dict(cu=MB + 1)),
+    ("ALIGNMENT", dict(cu=MB + 1)), ("ALIGNMENT", dict(ws=5 * MB + 8, ws_bytes=1 << 30)),
+    ("INVALID_ARG", dict(ws=3 * MB - 16, ws_bytes=32)),      # over out
 ]
 
 

@@ -297,3 +297,75 @@ def test_binding_refuses():
     with pytest.raises(s.SvdqError):
         s.attention(q, k[:, :1].expand(8, 2, 64), v)      # one head standing for two
     assert s.attention(q[:0], k[:0], v[:0]).shape == (0, 4, 64)
+
+
+def test_slots_that_sit_items_out():
+    """Causal items of which one half of the rows has nothing to do, beside
+    ones that keep it busy, many to a block: neither half runs ahead of the
+    other (short sequences have no second half; the last key tile of a divided
+    item has none for the first)."""
+    s = H.svdq()
+    for lens in ([700] + [100] * 60 + [2000] + [90] * 60, [128, 1500] * 6, [257] * 50):
+        cu = cu_of(lens)
+        q, k, v = make(cu[-1], 8, 2, 128, seed=17)
+        cut = torch.tensor(cu, dtype=torch.int32, device=DEV)
+        first = check(q, k, v, cu, True)
+        for _ in range(20):
+            got = s.attention(q, k, v, cut, True)
+            s.check_device_error()
+            assert torch.equal(got, first)
+
+
+def test_workspace_is_optional_and_checked():
+    """The C ABI with and without workspace: both within the tolerance; too
+    small a one is refused; the size query knows when none is of use."""
+    import ctypes
+    s = H.svdq()
+    lib = s._lib
+    T, D = 1500, 128
+    q, k, v = make(T, 2, 1, D, seed=18)
+    need = lib.svdq_attention_workspace_bytes(T, 2, D)
+    assert need > 0
+    for args in ((512, 2, D), (4352, 1 << 12, D), (0, 2, D), (T, 0, D), (T, 2, 0), (T, 2, 136), (T, 2, 60)):
+        assert lib.svdq_attention_workspace_bytes(*args) == 0
+    ws = torch.empty(need + 16, dtype=torch.uint8, device=DEV)
+    P = ctypes.c_void_p
+    for causal in (0, 1):
+        ref, tol = R.attention_ref(q, k, v, None, bool(causal), D ** -0.5)
+        for w, n, want in ((None, 0, s.SVDQ_OK), (ws, need, s.SVDQ_OK), (ws, need + 16, s.SVDQ_OK),
+                           (ws, need - 1, s.SVDQ_ERR_INVALID_ARG)):
+            out = torch.zeros_like(q)
+            st = lib.svdq_attention(s.BF16, P(q.data_ptr()), 2 * D, D, P(k.data_ptr()), D, D, P(v.data_ptr()), D, D, T,
+                                    2, 1, D, None, 1, causal, D ** -0.5, P(out.data_ptr()), 2 * D, D,
+                                    None if w is None else P(w.data_ptr()), n,
+                                    P(torch.cuda.current_stream().cuda_stream))
+            assert st == want
+            s.check_device_error()
+            if want == s.SVDQ_OK:
+                R.assert_within(out, ref, tol)
+            else:
+                assert (out == 0).all()
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("T,Hq,Hk", [(600, 1, 1), (1025, 1, 1), (3000, 1, 1), (9001, 1, 1), (2100, 5, 1)])
+def test_divided_items(T, Hq, Hk, causal):
+    """Few rows: their key tiles are divided among the blocks and joined."""
+    check(*make(T, Hq, Hk, 128, seed=T), None, causal)
+    check(*make(T, Hq, Hk, 72, HF, seed=T), cu_of([T // 3, 0, T - T // 3]), causal)
+
+
+@pytest.mark.parametrize("bad", ["inf", "nan"])
+def test_divided_items_keep_bad_keys_and_values_apart(bad):
+    T = 2000
+    q, k, v = make(T, 1, 1, 128, seed=19, by=0.5)
+    clean = H.svdq().attention(q, k, v, causal=True)
+    for at in (0, 640, 1100, 1900, 1999):
+        v2 = v.clone()
+        v2[at, 0, 5] = float(bad)
+        got = check(q, k, v2, None, True, rel=False)
+        assert torch.equal(got[:at], clean[:at])
+        k2 = k.clone()
+        k2[at, 0, 9] = float("nan")
+        got = H.svdq().attention(q, k2, v, causal=True)
+        assert torch.equal(got[:at], clean[:at]) and torch.isnan(got[at:]).all()
