@@ -365,7 +365,7 @@ int svdq_rope_turns(const int* axes, int n_axes, double theta, double* turns);
  *                 the call.
  *   q_weight, k_weight   [D] or NULL: no norm for that tensor.
  *   q_out, k_out  out, same shapes; each may be exactly its input.
- * Limits: n_axes <= 4, D % 8 == 0, D <= 256, R <= D, and R % 16 == 0 without
+ * Limits: n_axes <= 4, D % 8 == 0, D <= 256, R <= D, and R % 8 == 0 without
  * interleaving (else SVDQ_ERR_UNSUPPORTED). */
 int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, int Hq,
                  const uint16_t* k, int64_t k_stride_t, int64_t k_stride_h, int Hk, int T, int D,
@@ -383,18 +383,18 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
  * a row does not attend, whatever they hold (inf, NaN), do not reach it.
  *   q [T, Hq, D], k, v [T, Hk, D], out [T, Hq, D]  by strides (token, head).
  *   scale         finite and positive (usually 1 / sqrt(D)).
- *   workspace     NULL, or svdq_attention_workspace_bytes(T, Hq, D) bytes
- *                 (which depends on the device; 0: none is of use), 16-byte
- *                 aligned, overwritten.  With it, where rows are too few to
- *                 fill the device evenly, the key tiles are divided among
- *                 the SMs and the parts joined by a second kernel, in a
+ *   workspace     NULL, or at least svdq_attention_workspace_bytes(...) bytes
+ *                 (for this call's arguments, on this device; 0: none is of
+ *                 use), 16-byte aligned, overwritten.  With it, where rows
+ *                 are too few to fill the device, the key tiles are divided
+ *                 among the SMs and the parts joined by a second kernel, in a
  *                 fixed order.  Results repeat bit for bit for the same call
  *                 on the same device; with and without workspace they may
  *                 differ in the last bits of the fp32 sums.  Calls that may
  *                 overlap on the GPU need workspaces of their own.
  * Limits: Hq % Hk == 0, D % 8 == 0, D <= 128 (else SVDQ_ERR_SHAPE /
  * SVDQ_ERR_UNSUPPORTED). */
-size_t svdq_attention_workspace_bytes(int T, int Hq, int D);
+size_t svdq_attention_workspace_bytes(int T, int n_seqs, int Hq, int D, int causal);
 
 int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h,
                    const uint16_t* k, int64_t k_stride_t, int64_t k_stride_h, const uint16_t* v,

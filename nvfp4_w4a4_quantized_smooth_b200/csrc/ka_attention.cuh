@@ -50,30 +50,36 @@ constexpr int NUM_THREADS = 384;        // 2 x 4 softmax warps, 2 MMA, TMA, guar
 constexpr int MMA_WARP = 8, TMA_WARP = 10, GUARD_WARP = 11;
 constexpr uint32_t BOX_BYTES = ROWS * 128;   // 128 rows x 64 elements, 128-byte swizzle
 constexpr uint32_t TMEM_COLS = 512;
+constexpr int ITEMS = 4;                // work items that the warps are told in advance
 constexpr uint32_t TM_S = 0;            // S / P of slot s at 128 s
 constexpr uint32_t TM_O = 256;          // O of slot s at 256 + 128 s
-constexpr int MIN_RUN = 4;               // key tiles of a block's run, at least (split)
+constexpr int MIN_RUN = 6;               // places of a block's run, at least (split)
 constexpr int P_STEPS = 6;              // 16-key steps of P that are handed over first
 constexpr float RESCALE_LOG2 = 8.f;
-// Registers per thread of the softmax warps and of the others.
-constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 80;
+// Registers per thread of the softmax warps and of the others: all that the
+// block has (384 x 168).  The softmax loop is slower with fewer (208: 275 us
+// against 236 at 4352 x 30 heads), the others spill with fewer (224 / 56: 247).
+constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
 
 // NB: 64-element boxes per row (1: D <= 64, 2: D <= 128).
 template <int NB>
 struct Shape {
   static constexpr uint32_t TILE_BYTES = NB * BOX_BYTES;
-  static constexpr int STAGES = NB == 2 ? 5 : 10;
+  static constexpr int STAGES = NB == 2 ? 4 : 8;
   static constexpr uint32_t OFF_Q = 0;
   static constexpr uint32_t OFF_KV = 2 * TILE_BYTES;
-  static constexpr uint32_t OFF_BAR = OFF_KV + STAGES * TILE_BYTES;
+  // A warp's 32 rows x 128 bytes on the way out.
+  static constexpr uint32_t OFF_OUT = OFF_KV + STAGES * TILE_BYTES;
+  static constexpr uint32_t OFF_BAR = OFF_OUT + 8 * 4096;
   // full, empty, guard_go, guard_done [STAGES], q_full, q_empty, s_full[2],
   // p_full[2], p_rest[2], o_full[2], flags_full[2], flags_free[2], final[2],
-  // turn[2]
-  static constexpr int BARS = 4 * STAGES + 18;
+  // turn[2], item_full[ITEMS], item_empty[ITEMS]
+  static constexpr int BARS = 4 * STAGES + 18 + 2 * ITEMS;
   // Notes of the guard, one bit per key: [item parity][8 words].
   static constexpr uint32_t OFF_FLAGS = OFF_BAR + 8 * BARS;
   static constexpr uint32_t OFF_TMEM = OFF_FLAGS + 2 * 8 * 4;
-  static constexpr uint32_t USED = OFF_TMEM + 16;
+  static constexpr uint32_t OFF_ITEMS = OFF_TMEM + 16;   // 32 bytes each
+  static constexpr uint32_t USED = OFF_ITEMS + 32 * ITEMS;
   static constexpr uint32_t SMEM_BYTES = USED + 1024;   // 1024-byte alignment of the boxes
 };
 static_assert(Shape<2>::SMEM_BYTES <= 232448 && Shape<1>::SMEM_BYTES <= 232448, "");
@@ -81,7 +87,8 @@ static_assert(Shape<2>::SMEM_BYTES <= 232448 && Shape<1>::SMEM_BYTES <= 232448, 
 constexpr uint32_t SITE_TMA_Q = 0x50, SITE_TMA_KV = 0x51, SITE_MMA_Q = 0x52, SITE_MMA_KV = 0x53,
                    SITE_MMA_P = 0x54, SITE_MMA_GUARD = 0x55, SITE_SOFT_S = 0x56,
                    SITE_SOFT_O = 0x57, SITE_GUARD_V = 0x58, SITE_GUARD_FLAGS = 0x59,
-                   SITE_SOFT_FLAGS = 0x5A, SITE_MMA_TURN = 0x5B;
+                   SITE_SOFT_FLAGS = 0x5A, SITE_MMA_TURN = 0x5B, SITE_ITEM = 0x5C,
+                   SITE_TMA_ITEM = 0x5D;
 
 // What a block leaves of an item that it has only some key tiles of: a row's
 // reference, sum and unscaled O in the workspace, and this.
@@ -110,8 +117,7 @@ struct Params {
   int T, S, Hq, group, D;
   int causal;
   float scale_log2;         // scale * log2(e)
-  int split;                // items divided among the blocks
-  Workspace ws;             // split
+  Workspace ws;             // items divided among the blocks
 };
 
 // One work item: rows [q0, q0 + 256) of the sequence [begin, begin + len),
@@ -137,112 +143,113 @@ struct Item {
   }
 };
 
-// Walks a block's work.  Every warp runs its own copy.  Offsets are clamped to
-// [0, T] and to an increasing order, so that no entry of cu can lead outside
-// the tensors.
+// Walks a block's work: one warp does and tells the others.  Offsets are
+// clamped to [0, T] and to an increasing order, so that no entry of cu can
+// lead outside the tensors.
 //
 // Whole items: block b takes the items b, b + blocks, ... of all sequences
-// (causal: longest first within a sequence).  Split: the key tiles of all
-// items in one line are cut into equal runs, one per block, so that no SM
-// waits for another's last item and a few long rows still fill the device.
+// (causal: longest first within a sequence).  Split: the items of all
+// sequences lie in one line, each as long as its key tiles and one place more
+// for what an item costs by itself, and the line is cut into equal runs, one
+// per block.  (The host keeps the places below 2^31.)
+template <bool SPLIT>
 struct Items {
-  int s0 = 0;             // first sequence of the present group of 32
-  int64_t base = 0;       // items (split: key tiles) in front of it
-  int64_t at = 0, end = 0;
+  int s0 = -32;                   // the present group of 32 sequences, one per lane:
+  int begin_ = 0, len_ = 0;       //   its rows,
+  int incl_ = 0, size_ = 0;       //   places up to its end (within the group), its places
+  int base = 0, next_base = 0;    // places in front of the group, of the next
+  int at = 0, end = 0;
 
-  // Of a sequence: items, or key tiles of one head's items.
-  static __device__ __forceinline__ int64_t size(const Params& p, int len) {
-    const int64_t nt = (len + ITEM_ROWS - 1) / ITEM_ROWS;
-    if (!p.split) return nt * p.Hq;
-    const int64_t nk = (len + ROWS - 1) / ROWS;
+  // Of a sequence: items, or places of one head's items.
+  static __device__ __forceinline__ int size(const Params& p, int len) {
+    const int nt = (len + ITEM_ROWS - 1) / ITEM_ROWS;
+    if (!SPLIT) return nt * p.Hq;
+    const int nk = (len + ROWS - 1) / ROWS;
     // causal: 2, 4, 6, ... tiles, the last item one fewer where it has one slot
-    return (p.causal ? nt * (nt + 1) - (2 * nt - nk) : nt * nk) * p.Hq;
+    return (p.causal ? nt * (nt + 2) - (2 * nt - nk) : nt * (nk + 1)) * p.Hq;
   }
-  // The sequence that holds place w (which must not fall from call to call).
-  // Returns the place within the sequence, -1 behind the last.
-  __device__ __forceinline__ int64_t find(const Params& p, int64_t w, int& begin_out, int& len_out) {
-    const int lane = threadIdx.x & 31;
-    while (s0 < p.S) {
-      const int s = s0 + lane;
-      int begin = 0, len = 0;
-      if (s < p.S) {
-        begin = p.cu ? min(max(p.cu[s], 0), p.T) : 0;
-        len = (p.cu ? min(max(p.cu[s + 1], begin), p.T) : p.T) - begin;
-      }
-      const int64_t n = size(p, len);
-      int64_t incl = n;
+  __device__ __forceinline__ bool next_group(const Params& p) {
+    if (s0 + 32 >= p.S) return false;
+    s0 += 32;
+    base = next_base;
+    const int lane = threadIdx.x & 31, s = s0 + lane;
+    begin_ = len_ = 0;
+    if (s < p.S) {
+      begin_ = p.cu ? min(max(p.cu[s], 0), p.T) : 0;
+      len_ = (p.cu ? min(max(p.cu[s + 1], begin_), p.T) : p.T) - begin_;
+    }
+    incl_ = size_ = size(p, len_);
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t t = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-        if (lane >= o) incl += t;
-      }
-      const uint32_t mine = __ballot_sync(0xFFFFFFFFu, base + incl > w);
-      if (mine != 0u) {
-        const int src = __ffs(mine) - 1;
-        begin_out = __shfl_sync(0xFFFFFFFFu, begin, src);
-        len_out = __shfl_sync(0xFFFFFFFFu, len, src);
-        return __shfl_sync(0xFFFFFFFFu, w - base - (incl - n), src);
-      }
-      base += __shfl_sync(0xFFFFFFFFu, incl, 31);
-      s0 += 32;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int t = __shfl_up_sync(0xFFFFFFFFu, incl_, o);
+      if (lane >= o) incl_ += t;
     }
-    return -1;
-  }
-  // Split: the item at place w of the line of key tiles, and the place in it.
-  __device__ __forceinline__ bool locate(const Params& p, int64_t w, Item& it) {
-    const int64_t r = find(p, w, it.begin, it.len);
-    if (r < 0) return false;
-    const int64_t per = size(p, it.len) / p.Hq;
-    it.head = static_cast<int>(r / per);
-    const int64_t r2 = r - it.head * per;
-    if (p.causal) {
-      // i (i + 1) tiles in front of item i
-      int64_t i = static_cast<int64_t>((sqrtf(4.f * static_cast<float>(r2) + 1.f) - 1.f) * 0.5f);
-      while (i > 0 && i * (i + 1) > r2) --i;
-      while ((i + 1) * (i + 2) <= r2) ++i;
-      it.q0 = static_cast<int>(i) * ITEM_ROWS;
-      it.ka = static_cast<int>(r2 - i * (i + 1));
-    } else {
-      const int nk = it.key_tiles();
-      it.q0 = static_cast<int>(r2 / nk) * ITEM_ROWS;
-      it.ka = static_cast<int>(r2 % nk);
-    }
+    next_base = base + __shfl_sync(0xFFFFFFFFu, incl_, 31);
     return true;
   }
-  // Where block b's run begins: the equal share, moved to an item's edge where
-  // one is near (two partial results less).
-  static __device__ __forceinline__ int64_t edge(const Params& p, int64_t w, int64_t total, int64_t run) {
+  // The sequence that holds place w (which must not fall from call to call):
+  // the place within it, -1 behind the last.
+  __device__ __forceinline__ int find(const Params& p, int w, Item& it) {
+    while (w >= next_base)
+      if (!next_group(p)) return -1;
+    const int src = __ffs(__ballot_sync(0xFFFFFFFFu, base + incl_ > w)) - 1;
+    it.begin = __shfl_sync(0xFFFFFFFFu, begin_, src);
+    it.len = __shfl_sync(0xFFFFFFFFu, len_, src);
+    return w - base - __shfl_sync(0xFFFFFFFFu, incl_ - size_, src);
+  }
+  // Split: the item at place w, and w's place in it.
+  __device__ __forceinline__ int locate(const Params& p, int w, Item& it) {
+    const int r = find(p, w, it);
+    if (r < 0) return -1;
+    const int per = size(p, it.len) / p.Hq;
+    it.head = r / per;
+    const int r2 = r - it.head * per;
+    if (p.causal) {
+      // i (i + 2) places in front of item i
+      int i = static_cast<int>(sqrtf(static_cast<float>(r2) + 1.f)) - 1;
+      while (i > 0 && i * (i + 2) > r2) --i;
+      while ((i + 1) * (i + 3) <= r2) ++i;
+      it.q0 = i * ITEM_ROWS;
+      return r2 - i * (i + 2);
+    }
+    const int n = it.key_tiles() + 1;
+    it.q0 = r2 / n * ITEM_ROWS;
+    return r2 % n;
+  }
+  // Where a run begins that should begin at w: at an item's edge where one is
+  // near (two partial results less).
+  __device__ __forceinline__ int edge(const Params& p, int w, int total, int run) {
     if (w >= total) return total;
-    Items f;
+    if (p.S > 32) s0 = -32, next_base = 0;   // from the first group on again
     Item it;
-    f.locate(p, w, it);
-    const int n = it.all_tiles(p.causal);
-    const int64_t near = max(static_cast<int64_t>(1), run / 16);
-    if (it.ka <= near) return w - it.ka;
-    if (n - it.ka <= near) return w + n - it.ka;
-    return w;
+    const int r = locate(p, w, it), n = it.all_tiles(p.causal) + 1;
+    const int near = 1 + max(1, run / 16);
+    return r <= near ? w - r : n - r < near ? w + n - r : w;
   }
   __device__ __forceinline__ void start(const Params& p) {
     at = blockIdx.x;
-    if (!p.split) return;
-    int b, l;
-    Items all;
-    all.find(p, INT64_MAX, b, l);
-    const int64_t total = all.base;
-    const int64_t run = max(static_cast<int64_t>(MIN_RUN), (total + gridDim.x - 1) / gridDim.x);
-    at = edge(p, blockIdx.x * run, total, run);
-    end = edge(p, (blockIdx.x + 1) * run, total, run);
+    if (!SPLIT) return;
+    while (next_group(p)) {
+    }
+    const int total = next_base;
+    const int run = max(MIN_RUN, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
+    const int64_t w = static_cast<int64_t>(blockIdx.x) * run;
+    end = edge(p, static_cast<int>(min(w + run, static_cast<int64_t>(total))), total, run);
+    at = edge(p, static_cast<int>(min(w, static_cast<int64_t>(total))), total, run);
+    if (p.S > 32) s0 = -32, next_base = 0;
   }
   __device__ __forceinline__ bool get(const Params& p, Item& it) {
-    if (p.split) {
-      if (at >= end || !locate(p, at, it)) return false;
-      const int64_t left = end - at;
+    if (SPLIT) {
+      if (at >= end) return false;
+      const int r = locate(p, at, it);
+      if (r < 0) return false;
       const int n = it.all_tiles(p.causal);
-      it.kb = n - it.ka <= left ? n : it.ka + static_cast<int>(left);
-      at += it.kb - it.ka;
+      it.ka = max(0, r - 1);
+      it.kb = min(n, end - at + r - 1);
+      at += 1 + it.kb - r;
       return true;
     }
-    const int r = static_cast<int>(find(p, at, it.begin, it.len));
+    const int r = find(p, at, it);
     if (r < 0) return false;
     at += gridDim.x;
     const int nt = (it.len + ITEM_ROWS - 1) / ITEM_ROWS;
@@ -268,21 +275,13 @@ __device__ __forceinline__ void set_max_regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// ex2 that is computed where it stands (the compiler would move it behind the
-// test of the maximum, where alone its result is used).
-__device__ __forceinline__ float ex2_here(float y) {
-  float r;
-  asm volatile("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(y));
-  return r;
-}
-
 template <bool BF16>
 __device__ __forceinline__ bool is_nonfinite16(uint32_t e) {
   constexpr uint32_t m = BF16 ? 0x7F80u : 0x7C00u;
   return (e & m) == m;
 }
 
-template <bool BF16, int NB>
+template <bool BF16, int NB, bool SPLIT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attention_kernel(const __grid_constant__ CUtensorMap tm_q,
                      const __grid_constant__ CUtensorMap tm_k,
@@ -314,6 +313,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   auto flags_free = [&](int b) { return bar(4 * STAGES + 12 + b); };
   const uint32_t final_bar = bar(4 * STAGES + 14);
   const uint32_t turn_bar = bar(4 * STAGES + 16);
+  auto item_full = [&](uint32_t i) { return bar(4 * STAGES + 18 + i % ITEMS); };
+  auto item_empty = [&](uint32_t i) { return bar(4 * STAGES + 18 + ITEMS + i % ITEMS); };
+  const uint32_t s_items = sb + S_::OFF_ITEMS;
   auto s_q = [&](int s) { return sb + S_::OFF_Q + s * S_::TILE_BYTES; };
   auto s_kv = [&](uint32_t s) { return sb + S_::OFF_KV + s * S_::TILE_BYTES; };
   uint32_t* flags = reinterpret_cast<uint32_t*>(smem + S_::OFF_FLAGS);
@@ -339,6 +341,10 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     mbar_init(final_bar + 8, 1);
     mbar_init(turn_bar, 1);
     mbar_init(turn_bar + 8, 1);
+    for (int i = 0; i < ITEMS; ++i) {
+      mbar_init(item_full(i), 1);
+      mbar_init(item_empty(i), 11);   // every warp but the one that writes them
+    }
     fence_mbar_init();
   }
   if (warp == MMA_WARP) {
@@ -358,16 +364,43 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
   griddep_wait();
   griddep_launch_dependents();
 
-  Items items;
-  Item it;
-  items.start(p);
+  Item it = {};
+  uint32_t n = 0;   // items so far
+  // The next item, as the TMA warp has written it down; false behind the last.
+  auto next_item = [&]() {
+    if (!__all_sync(0xFFFFFFFFu, svdq_wait(item_full(n), (n / ITEMS) & 1u, SITE_ITEM))) return false;
+    const uint32_t at = s_items + 32 * (n % ITEMS);
+    uint32_t w[6];
+    ld_shared_v4(at, w[0], w[1], w[2], w[3]);
+    ld_shared_v2(at + 16, w[4], w[5]);
+    // (by shuffle, as the warp's number: loops over them are then uniform)
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = __shfl_sync(0xFFFFFFFFu, w[i], 0);
+    it.begin = w[0], it.len = w[1], it.q0 = w[2], it.head = w[3];
+    it.ka = SPLIT ? w[4] : 0;
+    it.kb = SPLIT ? w[5] : it.all_tiles(p.causal);
+    if (lane == 0) mbar_arrive(item_empty(n));
+    return it.len > 0;
+  };
   if (warp >= MMA_WARP) {
     set_max_regs_down<OTHER_REGS>();
     if (warp == TMA_WARP) {
       // ------------------------------------------------------------ TMA --
-      uint32_t kv = 0, n = 0;   // ring uses, items
+      uint32_t kv = 0;   // ring uses
       bool ok = true;
-      for (; ok && items.get(p, it); ++n) {
+      Items<SPLIT> items;
+      items.start(p);
+      for (bool more = true; more && ok; ++n) {
+        more = items.get(p, it);
+        ok = __all_sync(0xFFFFFFFFu, svdq_wait(item_empty(n), ((n / ITEMS) & 1u) ^ 1u, SITE_TMA_ITEM));
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t at = s_items + 32 * (n % ITEMS);
+          st_shared_v4(at, it.begin, more ? it.len : 0, it.q0, it.head);
+          st_shared_v4(at + 16, it.ka, it.kb, 0, 0);
+          mbar_arrive(item_full(n));
+        }
+        if (!more) break;
         if (lane == 0) {
           const int kh = it.head / p.group;
           ok = svdq_wait(q_empty, (n & 1u) ^ 1u, SITE_TMA_Q);
@@ -423,7 +456,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       const uint32_t b_s = s_full(s), b_p = p_full(s), b_rest = p_rest(s), b_o = o_full(s);
       uint32_t st = 0, ph = 0;          // next use of the ring: stage, parity
       uint32_t guards = 0;              // parity of the guarded uses, by stage
-      uint32_t n = 0, np = 0;           // items, P tiles
+      uint32_t np = 0;                  // P tiles
       uint32_t turn = s ^ 1u;           // parity of the turns (slot 0 has the first)
       bool ok = true;
       auto wait = [&](uint32_t b, uint32_t parity, uint32_t site) {
@@ -433,11 +466,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       auto next = [&]() {
         if (++st == STAGES) st = 0, ph ^= 1u;
       };
-      for (; ok && items.get(p, it); ++n) {
-        const int mine = it.end(s, p.causal);   // where this slot's key tiles end
-        const int last = it.key_tiles() - 1;
-        const int last_steps = (it.len - last * ROWS + 15) / 16;   // 16-key steps of the last tile
-        const int guard_from = it.guard_from(p.causal);
+      for (; ok && next_item(); ++n) {
+        // (tiles by their number from ka on: loops from zero)
+        const int tiles = it.kb - it.ka;
+        const int mine = it.end(s, p.causal) - it.ka;   // this slot's
+        const int last = it.key_tiles() - 1 - it.ka;    // the sequence's last
+        const int last_steps = (it.len % ROWS + ROWS - 1) % ROWS / 16 + 1;   // 16-key steps of that one
+        const int guard_from = it.guard_from(p.causal) - it.ka;
         // S of tile j from stage `at`; the other slot's turn begins while the
         // last products are issued.
         auto qk = [&](int j, uint32_t at, bool pass) {
@@ -456,19 +491,19 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             mbar_arrive(turn_bar + 8 * (s ^ 1));
           }
           tc_commit_by(leader, empty_bar(at));
-          if (j == it.kb - 1) tc_commit_by(leader, q_empty);
+          if (j == tiles - 1) tc_commit_by(leader, q_empty);
         };
         wait(q_full, n & 1u, SITE_MMA_Q);
         wait(full_bar(st), ph, SITE_MMA_KV);
         tc_fence_after();
         if (!ok) break;
-        qk(it.ka, st, false);
+        qk(0, st, false);
         next();
-        for (int j = it.ka; j < it.kb; ++j) {
+        for (int j = 0; j < tiles; ++j) {
           // All that the turn's products need is there before it is taken.
           const uint32_t sv = st;
           const uint64_t dv = desc_v + TILE_16 * sv;
-          const bool more = j + 1 < it.kb;
+          const bool more = j + 1 < tiles;
           wait(full_bar(sv), ph, SITE_MMA_KV);
           if (j >= guard_from) {
             wait(guard_done(sv), (guards >> sv) & 1u, SITE_MMA_GUARD);
@@ -492,7 +527,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
             for (int c = 0; c < P_STEPS; ++c)
               if (c < steps)
-                mma_f16_ts_by(leader, tm_o, tm_s + 8 * c, dv + 128 * c, id_o, c == 0 ? j != it.ka : 1u);
+                mma_f16_ts_by(leader, tm_o, tm_s + 8 * c, dv + 128 * c, id_o, c == 0 ? j != 0 : 1u);
             wait(b_rest, np++ & 1u, SITE_MMA_P);
             tc_fence_after();
             if (!ok) break;
@@ -514,10 +549,11 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       __syncwarp();
     } else {
       // ---------------------------------------------------------- guard --
-      uint32_t kv = 0, n = 0, phases = 0;
-      Meta meta[2] = {};   // split: this block's partial results
+      uint32_t kv = 0, phases = 0;
+      if (SPLIT && lane < 2) p.ws.meta[2 * blockIdx.x + lane].valid = 0;   // no partial results yet
+      __syncwarp();
       bool ok = true;
-      for (; ok && items.get(p, it); ++n) {
+      for (; ok && next_item(); ++n) {
         uint32_t* f = flags + 8 * (n & 1);
         if (p.causal) {
           // the epilogues of the item before last have read these words
@@ -573,16 +609,12 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         }
         if (ok && p.causal && lane == 0) mbar_arrive(flags_full(n & 1));
         kv += 2 * (it.kb - it.ka);
-        if (p.split && lane == 0 && !it.whole(p.causal)) {
-          Meta& m = meta[it.ka > 0 ? 0 : 1];
+        if (SPLIT && lane == 0 && !it.whole(p.causal)) {
+          Meta& m = p.ws.meta[2 * blockIdx.x + (it.ka > 0 ? 0 : 1)];
           m.valid = 1;
           m.last = it.kb == it.all_tiles(p.causal);
           m.begin = it.begin, m.len = it.len, m.q0 = it.q0, m.head = it.head;
         }
-      }
-      if (p.split && lane == 0) {
-        p.ws.meta[2 * blockIdx.x] = meta[0];
-        p.ws.meta[2 * blockIdx.x + 1] = meta[1];
       }
     }
   } else {
@@ -594,21 +626,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     const uint32_t tm_o = lane_base + TM_O + ROWS * slot;
     const int r = (warp & 3) * 32 + lane;   // row of the slot
     const float sc = p.scale_log2;
-    uint32_t ns = 0, no = 0, n = 0;         // S tiles, O tiles waited for, items
+    uint32_t ns = 0, no = 0;                // S tiles, O tiles waited for
     bool ok = true;
-    for (; ok && items.get(p, it); ++n) {
-      const int stop = it.end(slot, p.causal);   // its key tiles here are [ka, stop)
-      const bool whole = it.whole(p.causal);
+    for (; ok && next_item(); ++n) {
+      const int tiles = it.end(slot, p.causal) - it.ka;   // the slot's, from ka on
+      const bool whole = !SPLIT || it.whole(p.causal);
       auto notes = [&]() {   // the guard has been through this item
         return __all_sync(0xFFFFFFFFu, svdq_wait(flags_full(n & 1), (n >> 1) & 1u, SITE_SOFT_FLAGS)) != 0;
       };
       const int row = it.q0 + slot * ROWS + r;   // of the sequence
-      if (stop > it.ka) {
+      if (tiles > 0) {
+        const int row_keys = (p.causal ? min(it.len, row + 1) : it.len) - it.ka * ROWS;   // from ka on
         float m = -INFINITY;     // reference of the row, raw units of S
         float off = 0.f;         // -m in log2 units
         bool big = false;        // off is too large for one fma
         uint64_t sum2 = 0;       // of the weights, even and odd keys
-        for (int j = it.ka; j < stop; ++j) {
+        for (int j = 0; j < tiles; ++j) {
           ok = __all_sync(0xFFFFFFFFu, svdq_wait(s_full(slot), ns++ & 1u, SITE_SOFT_S));
           if (!ok) break;
           tc_fence_after();
@@ -617,7 +650,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(tm_s + 32 * c, x[c]);
           tmem_ld_wait();
           // keys at or behind `keys` are not this row's
-          const int keys = (p.causal ? min(it.len, row + 1) : it.len) - j * ROWS;
+          const int keys = row_keys - j * ROWS;
           if (__any_sync(0xFFFFFFFFu, keys < ROWS)) {
 #pragma unroll
             for (int c = 0; c < 4; ++c)
@@ -626,15 +659,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                 if (32 * c + e >= keys) x[c][e] = 0xFF800000u;   // -inf
           }
           // Weights 2^(x sc + off) of 32 keys, packed, and their sum.
-          auto weights = [&](const uint32_t (&xc)[32], uint32_t (&w16)[16], auto early) {
+          auto weights = [&](const uint32_t (&xc)[32], uint32_t (&w16)[16]) {
             const uint64_t sc2 = pk(sc, sc), off2 = pk(off, off);
             uint64_t sum[2] = {0, 0};
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
               float a, b;
               upk(fma2(pk(__uint_as_float(xc[2 * e]), __uint_as_float(xc[2 * e + 1])), sc2, off2), a, b);
-              a = decltype(early)::value ? ex2_here(a) : ex2_approx_ftz(a);
-              b = decltype(early)::value ? ex2_here(b) : ex2_approx_ftz(b);
+              a = ex2_approx_ftz(a);
+              b = ex2_approx_ftz(b);
               sum[e & 1] = add2(sum[e & 1], pk(a, b));
               w16[e] = pack2<BF16>(a, b);
             }
@@ -644,7 +677,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           // the maximum that says whether it still holds: it nearly always
           // does, so the maximum is off the way from S to P.
           uint32_t w16[16];
-          uint64_t part = weights(x[0], w16, Tag<true>());
+          uint64_t part = weights(x[0], w16);
           float t[4] = {m, m, m, m};
 #pragma unroll
           for (int c = 0; c < 4; ++c)
@@ -658,7 +691,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
               const float f = top == m ? 1.f : ex2_approx_ftz((m - top) * sc);
               m = top;
               sum2 = mul2(sum2, pk(f, f));
-              if (j > it.ka) {
+              if (j > 0) {
                 // O is idle here: the commit behind s_full also covers this
                 // slot's previous P V.
                 for (int c = 0; c < p.D; c += 16) {
@@ -685,13 +718,13 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
                 for (int e = 0; e < 32; ++e) x[c][e] = __float_as_uint(__uint_as_float(x[c][e]) - ref);
             }
-            part = weights(x[0], w16, Tag<false>());
+            part = weights(x[0], w16);
           }
           sum2 = add2(sum2, part);
           tmem_st_32x32b_x16(tm_s, w16);
 #pragma unroll
           for (int c = 1; c < 4; ++c) {
-            sum2 = add2(sum2, weights(x[c], w16, Tag<false>()));
+            sum2 = add2(sum2, weights(x[c], w16));
             tmem_st_32x32b_x16(tm_s + 16 * c, w16);
             if (c >= 2) {   // P_STEPS steps of 16 keys are there, then the rest
               tmem_st_wait();
@@ -718,46 +751,78 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 8; ++i) noted |= f[i];
         }
-        uint16_t* dst = p.out + static_cast<int64_t>(it.begin + row) * p.ost + it.head * p.osh;
-        const int prow = (2 * blockIdx.x + (it.ka > 0 ? 0 : 1)) * ITEM_ROWS + slot * ROWS + r;
-        float* part = p.ws.o + static_cast<size_t>(prow) * ((p.D + 15) / 16 * 16);
-        if (!whole) p.ws.ml[prow] = make_float2(m, l0 + l1);
-        for (int c = 0; c < p.D; c += 16) {
-          uint32_t o[16];
-          tmem_ld_32x32b_x16(tm_o + c, o);
-          tmem_ld_wait();
-          float v[16];
+        // Out by way of shared memory, 128 bytes of each of the warp's rows at
+        // a time, so that a store covers four whole lines instead of a piece
+        // of 32 (straight from the registers an item's rows took 4000 cycles
+        // of the memory pipe).  16-byte piece i of row k stands at i ^ (k & 7).
+        const uint32_t stage = sb + S_::OFF_OUT + 4096 * warp;
+        const int row0 = it.q0 + slot * ROWS + (warp & 3) * 32;   // the warp's first row
+        const int prow = (2 * blockIdx.x + (it.ka > 0 ? 0 : 1)) * ITEM_ROWS + slot * ROWS + (warp & 3) * 32;
+        const int dp = (p.D + 15) / 16 * 16;
+        if (!whole) p.ws.ml[prow + lane] = make_float2(m, l0 + l1);
+        const int width = whole ? 64 : 32;   // columns of 128 bytes
+        for (int c0 = 0; c0 < p.D; c0 += width) {
+          for (int c = c0; c < min(c0 + width, p.D); c += 16) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(tm_o + c, o);
+            tmem_ld_wait();
+            float v[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * inv;
-          if (noted != 0u) {
-            // Non-finite values of the diagonal tiles: into the rows that attend them.
-            for (int i = 0; i < 8; ++i) {
-              for (uint32_t b = f[i]; b != 0u; b &= b - 1) {
-                const int key = it.q0 + 32 * i + __ffs(b) - 1;
-                if (key > row) continue;
-                const uint16_t* src = p.v + static_cast<int64_t>(it.begin + key) * p.vst +
-                                      (it.head / p.group) * p.vsh + c;
+            for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(o[e]) * inv;
+            if (noted != 0u) {
+              // Non-finite values of the diagonal tiles: into the rows that attend them.
+              for (int i = 0; i < 8; ++i) {
+                for (uint32_t b = f[i]; b != 0u; b &= b - 1) {
+                  const int key = it.q0 + 32 * i + __ffs(b) - 1;
+                  if (key > row) continue;
+                  const uint16_t* src = p.v + static_cast<int64_t>(it.begin + key) * p.vst +
+                                        (it.head / p.group) * p.vsh + c;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                  if (c + e >= p.D) break;
-                  const uint32_t u = src[e];
-                  if (is_nonfinite16<BF16>(u))
-                    v[e] += BF16 ? __uint_as_float(u << 16)
-                                 : __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
+                  for (int e = 0; e < 16; ++e) {
+                    if (c + e >= p.D) break;
+                    const uint32_t u = src[e];
+                    if (is_nonfinite16<BF16>(u))
+                      v[e] += BF16 ? __uint_as_float(u << 16)
+                                   : __half2float(__ushort_as_half(static_cast<unsigned short>(u)));
+                  }
                 }
               }
             }
-          }
-          if (!whole) {
-            float4* o4 = reinterpret_cast<float4*>(part + c);
+            const uint32_t line = stage + 128 * lane;
+            if (whole) {
+              const int i = (c - c0) / 8;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o4[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-          } else if (row < it.len) {
-            const float (&a)[8] = reinterpret_cast<const float (&)[8]>(v[0]);
-            const float (&b)[8] = reinterpret_cast<const float (&)[8]>(v[8]);
-            *reinterpret_cast<uint4*>(dst + c) = pack8<BF16>(a);
-            if (c + 8 < p.D) *reinterpret_cast<uint4*>(dst + c + 8) = pack8<BF16>(b);
+              for (int k = 0; k < 2; ++k)
+                st_shared_v4(line + 16 * ((i + k) ^ (lane & 7)), pack2<BF16>(v[8 * k], v[8 * k + 1]),
+                             pack2<BF16>(v[8 * k + 2], v[8 * k + 3]), pack2<BF16>(v[8 * k + 4], v[8 * k + 5]),
+                             pack2<BF16>(v[8 * k + 6], v[8 * k + 7]));
+            } else {
+              const int i = (c - c0) / 4;
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                st_shared_v4(line + 16 * ((i + k) ^ (lane & 7)), __float_as_uint(v[4 * k]),
+                             __float_as_uint(v[4 * k + 1]), __float_as_uint(v[4 * k + 2]),
+                             __float_as_uint(v[4 * k + 3]));
+            }
           }
+          __syncwarp();
+          const int i = lane & 7;   // eight lanes a row, four rows a store
+          const bool in = whole ? c0 + 8 * i < p.D : c0 + 4 * i < dp;
+#pragma unroll
+          for (int k0 = 0; k0 < 32; k0 += 4) {
+            const int k = k0 + (lane >> 3);
+            uint4 w;
+            ld_shared_v4(stage + 128 * k + 16 * (i ^ (k & 7)), w.x, w.y, w.z, w.w);
+            if (!in) continue;
+            if (whole) {
+              if (row0 + k < it.len)
+                *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(it.begin + row0 + k) * p.ost +
+                                          it.head * p.osh + c0 + 8 * i) = w;
+            } else {
+              *reinterpret_cast<uint4*>(p.ws.o + static_cast<size_t>(prow + k) * dp + c0 + 4 * i) = w;
+            }
+          }
+          __syncwarp();
         }
         tc_fence_before();
       } else if (!whole && it.q0 + slot * ROWS < it.len) {
@@ -768,7 +833,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (p.causal) {
         // (also a slot that had nothing here waits for the notes: else it
         // would run ahead and arrive for a later item in this one's phase)
-        if (stop <= it.ka) ok = notes();
+        if (tiles <= 0) ok = notes();
         __syncwarp();
         if (lane == 0) mbar_arrive(flags_free(n & 1));
       }
@@ -790,7 +855,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
 // second one and goes on in the first ones of the blocks behind b, up to the
 // one that has its last key tile: the rows' references are brought to the
 // largest, sums and O added in that order, O divided by the sum.  Grid
-// (blocks, JOIN_PARTS): each block 256 / JOIN_PARTS rows, a warp per row.
+// (blocks, JOIN_PARTS): each block 256 / JOIN_PARTS rows, a warp four of them
+// at a time (it waits for memory once, not once a row).
 constexpr int JOIN_PARTS = 8;
 constexpr int JOIN_THREADS = 256;
 
@@ -807,43 +873,48 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Params p) {
     if (!m.valid) break;
     last = m.last;
   }
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  constexpr int R = ITEM_ROWS / JOIN_PARTS / (JOIN_THREADS / 32);   // rows of a warp
+  const int lane = threadIdx.x & 31;
+  const int r0 = blockIdx.y * (ITEM_ROWS / JOIN_PARTS) + (threadIdx.x >> 5) * R;
+  if (first.q0 + r0 >= first.len) return;
   const int dp = (p.D + 15) / 16 * 16;
   const int col = 4 * lane;
-  constexpr int ROWS_EACH = ITEM_ROWS / JOIN_PARTS;
-  for (int i = warp; i < ROWS_EACH; i += JOIN_THREADS / 32) {
-    const int r = blockIdx.y * ROWS_EACH + i;
-    const int row = first.q0 + r;
-    if (row >= first.len) break;
-    auto place = [&](int k) {
-      return static_cast<size_t>(k == 0 ? 2 * b + 1 : 2 * (b + k)) * ITEM_ROWS + r;
-    };
-    float top = -INFINITY;
-    for (int k = lane; k < parts; k += 32) top = fmaxf(top, p.ws.ml[place(k)].x);
+  auto place = [&](int k) { return static_cast<size_t>(k == 0 ? 2 * b + 1 : 2 * (b + k)) * ITEM_ROWS + r0; };
+  // (rows behind the sequence's end are computed too, from memory of the
+  // workspace that may not have been written, and not stored)
+  float top[R], l[R];
+  float4 o[R];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = 0; k < parts; ++k) {
-      const float2 ml = p.ws.ml[place(k)];
-      const float f = ml.x == top ? 1.f : ex2_approx_ftz((ml.x - top) * p.scale_log2);
-      l = fmaf(ml.y, f, l);
+  for (int i = 0; i < R; ++i) top[i] = -INFINITY, l[i] = 0.f, o[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k = 0; k < parts; ++k) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) top[i] = fmaxf(top[i], p.ws.ml[place(k) + i].x);
+  }
+#pragma unroll 2
+  for (int k = 0; k < parts; ++k) {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float2 ml = p.ws.ml[place(k) + i];
+      const float f = ml.x == top[i] ? 1.f : ex2_approx_ftz((ml.x - top[i]) * p.scale_log2);
+      l[i] = fmaf(ml.y, f, l[i]);
       // (a part without a key for the row has written no O)
       if (ml.x != -INFINITY && col < dp) {
-        const float4 v = *reinterpret_cast<const float4*>(p.ws.o + place(k) * dp + col);
-        o.x = fmaf(v.x, f, o.x);
-        o.y = fmaf(v.y, f, o.y);
-        o.z = fmaf(v.z, f, o.z);
-        o.w = fmaf(v.w, f, o.w);
+        const float4 v = *reinterpret_cast<const float4*>(p.ws.o + (place(k) + i) * dp + col);
+        o[i].x = fmaf(v.x, f, o[i].x);
+        o[i].y = fmaf(v.y, f, o[i].y);
+        o[i].z = fmaf(v.z, f, o[i].z);
+        o[i].w = fmaf(v.w, f, o[i].w);
       }
     }
-    const float inv = 1.f / l;
-    if (col < p.D) {
-      uint16_t* dst = p.out + static_cast<int64_t>(first.begin + row) * p.ost + first.head * p.osh + col;
-      *reinterpret_cast<uint2*>(dst) =
-          make_uint2(pack2<BF16>(o.x * inv, o.y * inv), pack2<BF16>(o.z * inv, o.w * inv));
-    }
+  }
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int row = first.q0 + r0 + i;
+    if (row >= first.len || col >= p.D) continue;
+    const float inv = 1.f / l[i];
+    uint16_t* dst = p.out + static_cast<int64_t>(first.begin + row) * p.ost + first.head * p.osh + col;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF16>(o[i].x * inv, o[i].y * inv),
+                                                pack2<BF16>(o[i].z * inv, o[i].w * inv));
   }
 }
 

@@ -1083,18 +1083,34 @@ RopeKernel rope_kernel(int D, bool pairs) {
   return pairs ? rope_qk_kernel<BF16, 32, true> : rope_qk_kernel<BF16, 32, false>;
 }
 
-template <bool BF16, int NB>
+using AttentionKernel = void (*)(const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                                 const svdq::ka::Params);
+
+template <bool BF16>
+AttentionKernel attention_instance(bool wide, bool split) {
+  using namespace svdq::ka;
+  return wide ? (split ? attention_kernel<BF16, 2, true> : attention_kernel<BF16, 2, false>)
+              : (split ? attention_kernel<BF16, 1, true> : attention_kernel<BF16, 1, false>);
+}
+
+uint32_t attention_smem(bool wide) {
+  return wide ? svdq::ka::Shape<2>::SMEM_BYTES : svdq::ka::Shape<1>::SMEM_BYTES;
+}
+
 int prepare_ka() {
   using namespace svdq::ka;
-  const auto fn = attention_kernel<BF16, NB>;
-  cudaFuncAttributes a;
-  if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           svdq::ka::Shape<NB>::SMEM_BYTES) != cudaSuccess ||
-      cudaFuncGetAttributes(&a, fn) != cudaSuccess)
-    return SVDQ_ERR_CUDA;
-  // The warp roles' register shares come out of the block's registers.
-  return a.numRegs * NUM_THREADS >= SOFTMAX_REGS * 256 + OTHER_REGS * 128 ? SVDQ_OK
-                                                                          : SVDQ_ERR_UNSUPPORTED;
+  for (bool wide : {false, true})
+    for (bool split : {false, true})
+      for (AttentionKernel fn : {attention_instance<false>(wide, split), attention_instance<true>(wide, split)}) {
+        cudaFuncAttributes a;
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 attention_smem(wide)) != cudaSuccess ||
+            cudaFuncGetAttributes(&a, fn) != cudaSuccess)
+          return SVDQ_ERR_CUDA;
+        // The warp roles' register shares come out of the block's registers.
+        if (a.numRegs * NUM_THREADS < SOFTMAX_REGS * 256 + OTHER_REGS * 128) return SVDQ_ERR_UNSUPPORTED;
+      }
+  return SVDQ_OK;
 }
 
 template <bool BF16, int VPT>
@@ -1124,22 +1140,26 @@ int block_setup(DeviceInfo* d) {
   if (!st) st = prepare_kn<true, 2>();
   if (!st) st = prepare_kn<false, 1>();
   if (!st) st = prepare_kn<false, 2>();
-  if (!st) st = prepare_ka<true, 1>();
-  if (!st) st = prepare_ka<true, 2>();
-  if (!st) st = prepare_ka<false, 1>();
-  if (!st) st = prepare_ka<false, 2>();
+  if (!st) st = prepare_ka();
   if (st) return st;
   d->block_ready = true;
   return SVDQ_OK;
 }
 
-// Whether the attention divides work items among the blocks: where there are
-// fewer than eight whole items per SM (a last, partly filled round of items
-// then costs more than an eighth), and more key tiles than a block's least
-// run (else no item is ever cut).
-bool ka_may_split(DeviceInfo* d, int T, int Hq) {
-  const int64_t items = (static_cast<int64_t>(T) + svdq::ka::ITEM_ROWS - 1) / svdq::ka::ITEM_ROWS * Hq;
-  return T > svdq::ka::MIN_RUN * svdq::ka::ROWS && items < static_cast<int64_t>(8) * d->num_sms;
+// Whether the attention divides work items among the blocks: where they are
+// fewer than the SMs and a run of an equal share is shorter than the longest
+// item by more than dividing and joining cost, about 18 key tiles' time.
+// (Measured with one sequence, divided against whole, D = 128: full, 8192
+// rows x 2 heads 70 us / 102 us, 4352 x 4 53 / 58, 4352 x 8 80 / 60; causal,
+// 16384 x 1 99 / 201, 8192 x 4 100 / 110, 2304 x 14 57 / 43.)
+bool ka_may_split(DeviceInfo* d, int T, int n_seqs, int Hq, int causal) {
+  namespace ka = svdq::ka;
+  const int64_t items = (static_cast<int64_t>(T) + ka::ITEM_ROWS - 1) / ka::ITEM_ROWS * Hq;
+  if (items >= d->num_sms) return false;
+  const int64_t tiles = T / n_seqs / ka::ROWS;                   // of a usual sequence's longest item
+  const int64_t share = items * (causal ? 1 : 2);                // twice the SMs' worth of work
+  return items * (T / ka::ROWS + 2) < INT_MAX &&
+         tiles * (2 * d->num_sms - share) > 2 * 18 * d->num_sms;
 }
 
 bool bad_norm(int kind) { return kind < 0 || kind > SVDQ_NORM_LAYER; }
@@ -1254,7 +1274,7 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
     R += axes[a];
   }
   if (R > D) return SVDQ_ERR_SHAPE;
-  if (D % 8 || D > svdq::kp::MAX_D || (!interleaved && R % 16) ||
+  if (D % 8 || D > svdq::kp::MAX_D || (!interleaved && R % 8) ||
       Hq + static_cast<int64_t>(Hk) > (1 << 16))
     return SVDQ_ERR_UNSUPPORTED;
   if (T == 0) return SVDQ_OK;
@@ -1344,11 +1364,11 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
   return launch_status();
 }
 
-size_t svdq_attention_workspace_bytes(int T, int Hq, int D) {
-  if (T < 1 || Hq < 1 || D < 8 || D % 8 || D > svdq::ka::MAX_D) return 0;
+size_t svdq_attention_workspace_bytes(int T, int n_seqs, int Hq, int D, int causal) {
+  if (T < 1 || n_seqs < 1 || Hq < 1 || D < 8 || D % 8 || D > svdq::ka::MAX_D) return 0;
   DeviceInfo* d = nullptr;
   if (device_setup(&d)) return 0;
-  if (!ka_may_split(d, T, Hq)) return 0;
+  if (!ka_may_split(d, T, n_seqs, Hq, causal)) return 0;
   return svdq::ka::Workspace::bytes(d->num_sms, (D + 15) / 16 * 16);
 }
 
@@ -1420,9 +1440,9 @@ int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_s
   const int64_t items = (static_cast<int64_t>(T) / ka::ITEM_ROWS + n_seqs) * Hq;
   unsigned grid = static_cast<unsigned>(items < d->num_sms ? items : d->num_sms);
   const int dp = (D + 15) / 16 * 16;
-  p.split = workspace && ka_may_split(d, T, Hq) ? 1 : 0;
+  const bool split = workspace && ka_may_split(d, T, n_seqs, Hq, causal);
   p.ws = {};
-  if (p.split) {
+  if (split) {
     grid = d->num_sms;
     if (workspace_bytes < ka::Workspace::bytes(grid, dp)) return SVDQ_ERR_INVALID_ARG;
     const size_t rows = static_cast<size_t>(2) * grid * ka::ITEM_ROWS;
@@ -1433,16 +1453,12 @@ int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_s
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr;
   const bool wide = D > 64;
-  pdl_config(&cfg, &attr, grid, ka::NUM_THREADS,
-             wide ? ka::Shape<2>::SMEM_BYTES : ka::Shape<1>::SMEM_BYTES, stream);
-  const cudaError_t e =
-      dtype == SVDQ_BF16
-          ? (wide ? cudaLaunchKernelEx(&cfg, ka::attention_kernel<true, 2>, tm_q, tm_k, tm_v, p)
-                  : cudaLaunchKernelEx(&cfg, ka::attention_kernel<true, 1>, tm_q, tm_k, tm_v, p))
-          : (wide ? cudaLaunchKernelEx(&cfg, ka::attention_kernel<false, 2>, tm_q, tm_k, tm_v, p)
-                  : cudaLaunchKernelEx(&cfg, ka::attention_kernel<false, 1>, tm_q, tm_k, tm_v, p));
-  if (e != cudaSuccess) return SVDQ_ERR_CUDA;
-  if (p.split) {
+  pdl_config(&cfg, &attr, grid, ka::NUM_THREADS, attention_smem(wide), stream);
+  if (cudaLaunchKernelEx(&cfg, dtype == SVDQ_BF16 ? attention_instance<true>(wide, split)
+                                                  : attention_instance<false>(wide, split),
+                         tm_q, tm_k, tm_v, p) != cudaSuccess)
+    return SVDQ_ERR_CUDA;
+  if (split) {
     pdl_config(&cfg, &attr, grid, ka::JOIN_THREADS, 0, stream);
     cfg.gridDim.y = ka::JOIN_PARTS;
     if ((dtype == SVDQ_BF16 ? cudaLaunchKernelEx(&cfg, ka::join_kernel<true>, p)

@@ -78,7 +78,7 @@ SIGNATURES = {
                           _P, _F, _P, _L, _L, _P, _L, _L, _P]),
     "svdq_attention": (_I, [_I, _P, _L, _L, _P, _L, _L, _P, _L, _L, _I, _I, _I, _I, _P, _I, _I,
                             _F, _P, _L, _L, _P, _SZ, _P]),
-    "svdq_attention_workspace_bytes": (_SZ, [_I, _I, _I]),
+    "svdq_attention_workspace_bytes": (_SZ, [_I, _I, _I, _I, _I]),
     "svdq_check_device_error": (_I, [_P]),
     "svdq_set_wait_timeout_ns": (_I, [ctypes.c_uint64]),
     "svdq_wait_probe": (_I, [_I, _P]),
@@ -406,34 +406,20 @@ _DTYPES = {torch.bfloat16: BF16, torch.float16: FP16}
 _NORMS = {None: NORM_NONE, "rms": NORM_RMS, "layer": NORM_LAYER}
 
 
-class _On:
-    """The device of a call's tensors (its index) made current, and its
-    stream: the given one, or the device's current one.  Outputs allocated
-    inside belong to that stream."""
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
-    __slots__ = ("index", "stream", "ctx")
 
-    def __init__(self, index: int, stream: Optional[torch.cuda.Stream]):
-        self.index = index
-        self.stream = stream
-        self.ctx = None
-        if stream is not None:
-            if stream.device.index != index:
-                raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
-            self.ctx = torch.cuda.stream(stream)       # also makes its device current
-        elif index != torch._C._cuda_getDevice():
-            self.ctx = torch.cuda.device(index)
-
-    def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
-        if self.stream is not None:
-            return self.stream.cuda_stream
-        return torch._C._cuda_getCurrentRawStream(self.index)
-
-    def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+def _on(index: int, stream: Optional[torch.cuda.Stream]):
+    """A context in which the stream (or, without one, the device of that
+    index) is the current one.  A call on another stream or device than the
+    current ones enters it and calls itself: its launch and the outputs it
+    allocates then belong there."""
+    if stream is None:
+        return torch.cuda.device(index)
+    if stream.device.index != index:
+        raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{index}")
+    return torch.cuda.stream(stream)
 
 
 def _need_like(t: torch.Tensor, dtype: torch.dtype, index: int, shape, name: str):
@@ -491,20 +477,38 @@ def norm_gate_residual(x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
     h and n may be given, also exactly x or y; rows in no sequence are left
     as they are."""
     code = _need_16bit(x, "x", 2)
+    index = x.get_device()
+    if stream is not None or index != _current_device():
+        with _on(index, stream):
+            return norm_gate_residual(x, y, gate=gate, scale=scale, shift=shift,
+                                      post_weight=post_weight, pre_weight=pre_weight, post=post,
+                                      pre=pre, eps=eps, gate_tanh=gate_tanh,
+                                      residual_scale=residual_scale, cu_seqlens=cu_seqlens, h=h,
+                                      n=n)
     if post not in _NORMS or pre not in _NORMS:
         raise ValueError('post and pre must be None, "rms" or "layer"')
-    shape, dtype, index = x.shape, x.dtype, x.get_device()
+    shape, dtype = x.shape, x.dtype
     T, C = shape
-    S = 1 if cu_seqlens is None else _need_cu(cu_seqlens, index)
+    S, cu = 1, None
+    if cu_seqlens is not None:
+        S, cu = _need_cu(cu_seqlens, index), cu_seqlens.data_ptr()
     ldx = _need_like(x, dtype, index, shape, "x")[0]
     py = pg = ps = pb = pw = qw = pn = ph = None
     ldy = ldg = lds = ldb = ldh = ldn = 0
     if y is not None:
         ldy = _need_like(y, dtype, index, shape, "y")[0]
         py = y.data_ptr()
+        if h is None:
+            h = torch.empty_like(x, memory_format=torch.contiguous_format)
+            ldh = C
+        else:
+            ldh = _need_like(h, dtype, index, shape, "h")[0]
+        ph = h.data_ptr()
     elif h is not None:
         raise ValueError("h needs y (without y it is x itself)")
+    kind = GATE_NONE
     if gate is not None:
+        kind = GATE_TANH if gate_tanh else GATE_LINEAR
         ldg = _need_like(gate, dtype, index, (S, C), "gate")[0]
         pg = gate.data_ptr()
     if scale is not None:
@@ -521,26 +525,20 @@ def norm_gate_residual(x: torch.Tensor, y: Optional[torch.Tensor] = None, *,
     if pre_weight is not None:
         _need_like(pre_weight, dtype, index, (C,), "pre_weight")
         qw = pre_weight.data_ptr()
-    want_n = pre is not None or scale is not None or shift is not None
-    with _On(index, stream) as s:
-        if y is not None:
-            if h is None:
-                h = x.new_empty((T, C))
-            ldh = _need_like(h, dtype, index, shape, "h")[0]
-            ph = h.data_ptr()
-        if n is None and want_n:
-            n = x.new_empty((T, C))
-        if n is not None:
-            ldn = _need_like(n, dtype, index, shape, "n")[0]
-            pn = n.data_ptr()
-        if T == 1:
-            ldx = ldy = ldh = ldn = C
-        _check(_lib.svdq_norm_gate_residual(
-            code, x.data_ptr(), ldx, py, ldy, T, C,
-            None if cu_seqlens is None else cu_seqlens.data_ptr(), S, _NORMS[post], pw,
-            GATE_NONE if gate is None else GATE_TANH if gate_tanh else GATE_LINEAR, pg, ldg,
-            residual_scale, _NORMS[pre], qw, ps, lds, pb, ldb, eps, ph, ldh, pn, ldn, s),
-            "svdq_norm_gate_residual")
+    if n is not None:
+        ldn = _need_like(n, dtype, index, shape, "n")[0]
+        pn = n.data_ptr()
+    elif pre is not None or scale is not None or shift is not None:
+        n = torch.empty_like(x, memory_format=torch.contiguous_format)
+        ldn, pn = C, n.data_ptr()
+    if T == 1:
+        ldx = ldy = ldh = ldn = C
+    st = _lib.svdq_norm_gate_residual(
+        code, x.data_ptr(), ldx, py, ldy, T, C, cu, S, _NORMS[post], pw, kind, pg, ldg,
+        residual_scale, _NORMS[pre], qw, ps, lds, pb, ldb, eps, ph, ldh, pn, ldn,
+        _raw_stream(index))
+    if st != SVDQ_OK:
+        raise SvdqError(st, "svdq_norm_gate_residual")
     return (x if y is None else h), n
 
 
@@ -577,7 +575,11 @@ def rope_qk(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: tor
     if first is None:
         raise ValueError("rope_qk needs q or k")
     code = _need_16bit(first, "q" if q is not None else "k", 3)
-    dtype, index = first.dtype, first.get_device()
+    index = first.get_device()
+    if stream is not None or index != _current_device():
+        with _on(index, stream):
+            return rope_qk(q, k, positions, plan, q_weight, k_weight, eps, q_out, k_out)
+    dtype = first.dtype
     T, _, D = first.shape
     if D != plan.head_dim:
         raise ValueError(f"heads of {D}, the plan is for {plan.head_dim}")
@@ -593,36 +595,34 @@ def rope_qk(q: Optional[torch.Tensor], k: Optional[torch.Tensor], positions: tor
     Hq = Hk = 0
     pq = pk = pqo = pko = wq = wk = None
     qs = ks = qos = kos = (0, 0)
-    with _On(index, stream) as s:
-        if q is not None:
-            Hq = q.shape[1]
-            shape = (T, Hq, D)
-            qs = _need_like(q, dtype, index, shape, "q")
-            if q_out is None:
-                q_out = q.new_empty((T, Hq, D))
-            qos = _need_like(q_out, dtype, index, shape, "q_out")
-            pq, pqo = q.data_ptr(), q_out.data_ptr()
-        if k is not None:
-            if k.dim() != 3:
-                raise ValueError("k must have 3 dims")
-            Hk = k.shape[1]
-            shape = (T, Hk, D)
-            ks = _need_like(k, dtype, index, shape, "k")
-            if k_out is None:
-                k_out = k.new_empty(shape)
-            kos = _need_like(k_out, dtype, index, shape, "k_out")
-            pk, pko = k.data_ptr(), k_out.data_ptr()
-        if q_weight is not None:
-            _need_like(q_weight, dtype, index, (D,), "q_weight")
-            wq = q_weight.data_ptr()
-        if k_weight is not None:
-            _need_like(k_weight, dtype, index, (D,), "k_weight")
-            wk = k_weight.data_ptr()
-        _check(_lib.svdq_rope_qk(code, pq, qs[0], qs[1], Hq, pk, ks[0], ks[1], Hk, T, D,
-                                 positions.data_ptr(), ldp if T > 1 else A, plan._axes, A,
-                                 plan._turns, plan._pairs, wq, wk, eps, pqo, qos[0], qos[1], pko,
-                                 kos[0], kos[1], s),
-               "svdq_rope_qk")
+    if q is not None:
+        Hq = q.shape[1]
+        qs = _need_like(q, dtype, index, (T, Hq, D), "q")
+        if q_out is None:
+            q_out = q.new_empty((T, Hq, D))
+        qos = _need_like(q_out, dtype, index, (T, Hq, D), "q_out")
+        pq, pqo = q.data_ptr(), q_out.data_ptr()
+    if k is not None:
+        if k.dim() != 3:
+            raise ValueError("k must have 3 dims")
+        Hk = k.shape[1]
+        ks = _need_like(k, dtype, index, (T, Hk, D), "k")
+        if k_out is None:
+            k_out = k.new_empty((T, Hk, D))
+        kos = _need_like(k_out, dtype, index, (T, Hk, D), "k_out")
+        pk, pko = k.data_ptr(), k_out.data_ptr()
+    if q_weight is not None:
+        _need_like(q_weight, dtype, index, (D,), "q_weight")
+        wq = q_weight.data_ptr()
+    if k_weight is not None:
+        _need_like(k_weight, dtype, index, (D,), "k_weight")
+        wk = k_weight.data_ptr()
+    st = _lib.svdq_rope_qk(code, pq, qs[0], qs[1], Hq, pk, ks[0], ks[1], Hk, T, D,
+                           positions.data_ptr(), ldp if T > 1 else A, plan._axes, A, plan._turns,
+                           plan._pairs, wq, wk, eps, pqo, qos[0], qos[1], pko, kos[0], kos[1],
+                           _raw_stream(index))
+    if st != SVDQ_OK:
+        raise SvdqError(st, "svdq_rope_qk")
     return q_out, k_out
 
 
@@ -638,30 +638,42 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     itself, only backwards with causal.  scale None: 1 / sqrt(D).  Rows in
     no sequence are left as they are in out."""
     code = _need_16bit(q, "q", 3)
+    index = q.get_device()
+    if stream is not None or index != _current_device():
+        with _on(index, stream):
+            return attention(q, k, v, cu_seqlens, causal, scale, out)
     if k.dim() != 3:
         raise ValueError("k must have 3 dims")
-    dtype, index, shape = q.dtype, q.get_device(), q.shape
+    dtype, shape = q.dtype, q.shape
     T, Hq, D = shape
-    Hk = k.shape[1]
+    kv_shape = k.shape
+    Hk = kv_shape[1]
+    if kv_shape != (T, Hk, D):
+        raise ValueError(f"k must have shape {[T, Hk, D]}, got {list(kv_shape)}")
     qs = _need_like(q, dtype, index, shape, "q")
-    ks = _need_like(k, dtype, index, (T, Hk, D), "k")
-    vs = _need_like(v, dtype, index, (T, Hk, D), "v")
-    S = 1 if cu_seqlens is None else _need_cu(cu_seqlens, index)
+    ks = _need_like(k, dtype, index, kv_shape, "k")
+    vs = _need_like(v, dtype, index, kv_shape, "v")
+    S, cu = 1, None
+    if cu_seqlens is not None:
+        S, cu = _need_cu(cu_seqlens, index), cu_seqlens.data_ptr()
     if scale is None:
         scale = D ** -0.5 if D else 1.0
-    with _On(index, stream) as s:
-        if out is None:
-            out = q.new_empty((T, Hq, D))
-        os_ = _need_like(out, dtype, index, shape, "out")
-        ws, size = None, _lib.svdq_attention_workspace_bytes(T, Hq, D) if T > 512 else 0
+    if out is None:
+        out = q.new_empty((T, Hq, D))
+        so, sh = Hq * D, D
+    else:
+        so, sh, _ = _need_like(out, dtype, index, shape, "out")
+    pw, size = None, 0
+    if T > 2048:                     # no workspace is of use to fewer rows
+        size = _lib.svdq_attention_workspace_bytes(T, S, Hq, D, 1 if causal else 0)
         if size:
             ws = torch.empty(size, dtype=torch.uint8, device=q.device)
-        _check(_lib.svdq_attention(
-            code, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0],
-            vs[1], T, Hq, Hk, D, None if cu_seqlens is None else cu_seqlens.data_ptr(), S,
-            1 if causal else 0, scale, out.data_ptr(), os_[0], os_[1],
-            None if ws is None else ws.data_ptr(), size, s),
-            "svdq_attention")
+            pw = ws.data_ptr()
+    st = _lib.svdq_attention(code, q.data_ptr(), qs[0], qs[1], k.data_ptr(), ks[0], ks[1],
+                             v.data_ptr(), vs[0], vs[1], T, Hq, Hk, D, cu, S, 1 if causal else 0,
+                             scale, out.data_ptr(), so, sh, pw, size, _raw_stream(index))
+    if st != SVDQ_OK:
+        raise SvdqError(st, "svdq_attention")
     return out
 
 

@@ -104,7 +104,7 @@ ROPE_BAD = [
     ("SHAPE", dict(T=-1)), ("SHAPE", dict(Hq=-1)), ("SHAPE", dict(D=0)), ("SHAPE", dict(ldp=2)),
     ("SHAPE", dict(qst=32)), ("SHAPE", dict(qosh=32)),
     ("UNSUPPORTED", dict(D=68)), ("UNSUPPORTED", dict(D=264, qst=1024, qsh=264)),
-    ("UNSUPPORTED", dict(axes=(16, 24), il=0)),          # R = 40 in halves
+    ("UNSUPPORTED", dict(axes=(16, 20), il=0)),          # R = 36 in halves
     ("ALIGNMENT", dict(q=MB + 2)), ("ALIGNMENT", dict(qst=196)), ("ALIGNMENT", dict(qosh=68, qost=136)),
     ("ALIGNMENT", dict(qw=8 * MB + 2)),
 ]

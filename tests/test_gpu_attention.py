@@ -322,11 +322,12 @@ def test_workspace_is_optional_and_checked():
     import ctypes
     s = H.svdq()
     lib = s._lib
-    T, D = 1500, 128
+    T, D = 4000, 128
     q, k, v = make(T, 2, 1, D, seed=18)
-    need = lib.svdq_attention_workspace_bytes(T, 2, D)
+    need = lib.svdq_attention_workspace_bytes(T, 1, 2, D, 0)
     assert need > 0
-    for args in ((512, 2, D), (4352, 1 << 12, D), (0, 2, D), (T, 0, D), (T, 2, 0), (T, 2, 136), (T, 2, 60)):
+    for args in ((512, 1, 2, D, 1), (4352, 1, 1 << 12, D, 0), (4000, 40, 2, D, 1), (0, 1, 2, D, 0), (T, 1, 0, D, 0),
+                 (T, 1, 2, 0, 0), (T, 1, 2, 136, 0), (T, 1, 2, 60, 0), (T, 0, 2, D, 0)):
         assert lib.svdq_attention_workspace_bytes(*args) == 0
     ws = torch.empty(need + 16, dtype=torch.uint8, device=DEV)
     P = ctypes.c_void_p
@@ -348,19 +349,22 @@ def test_workspace_is_optional_and_checked():
 
 
 @pytest.mark.parametrize("causal", [False, True])
-@pytest.mark.parametrize("T,Hq,Hk", [(600, 1, 1), (1025, 1, 1), (3000, 1, 1), (9001, 1, 1), (2100, 5, 1)])
+@pytest.mark.parametrize("T,Hq,Hk", [(2600, 1, 1), (3000, 1, 1), (3333, 2, 1), (9001, 1, 1), (5000, 3, 1)])
 def test_divided_items(T, Hq, Hk, causal):
     """Few rows: their key tiles are divided among the blocks and joined."""
+    assert H.svdq()._lib.svdq_attention_workspace_bytes(T, 1, Hq, 128, int(causal)) > 0
     check(*make(T, Hq, Hk, 128, seed=T), None, causal)
-    check(*make(T, Hq, Hk, 72, HF, seed=T), cu_of([T // 3, 0, T - T // 3]), causal)
+    check(*make(T, Hq, Hk, 72, HF, seed=T), cu_of([T - 100], 50), causal)
+    many = cu_of([T // 2, 0, 1, T - T // 2 - 1])     # short ones beside: if it is divided at all
+    check(*make(T, Hq, Hk, 128, seed=T), many, causal)
 
 
 @pytest.mark.parametrize("bad", ["inf", "nan"])
 def test_divided_items_keep_bad_keys_and_values_apart(bad):
-    T = 2000
+    T = 4000
     q, k, v = make(T, 1, 1, 128, seed=19, by=0.5)
     clean = H.svdq().attention(q, k, v, causal=True)
-    for at in (0, 640, 1100, 1900, 1999):
+    for at in (0, 640, 1100, 2900, 3999):
         v2 = v.clone()
         v2[at, 0, 5] = float(bad)
         got = check(q, k, v2, None, True, rel=False)

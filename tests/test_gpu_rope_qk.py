@@ -53,10 +53,11 @@ def check(T, Hq, Hk, D, axes, pairs=True, norm=True, dtype=BF, far=1000, theta=2
 @pytest.mark.parametrize("norm", [True, False])
 @pytest.mark.parametrize("D,axes", [(128, (32, 48, 48)), (64, (16, 24, 24)), (128, (16, 16)), (8, (4, 4)),
                                     (96, (32, 32, 32)), (80, (16, 32, 16)), (256, (64, 64, 128)), (16, (16,)),
-                                    (136, (32, 96)), (128, (32, 32, 32, 32))])
+                                    (136, (32, 96)), (128, (32, 32, 32, 32)), (64, (8, 24, 24)), (64, (16, 24)),
+                                    (24, (8,)), (88, (40, 48))])
 def test_axes_and_widths(dtype, pairs, norm, D, axes):
-    if not pairs and sum(axes) % 16:
-        pytest.skip("halves need 16 | R")
+    if not pairs and sum(axes) % 8:
+        pytest.skip("halves need 8 | R")
     check(33, 3, 2, D, axes, pairs, norm, dtype)
 
 
