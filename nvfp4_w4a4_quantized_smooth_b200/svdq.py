@@ -720,3 +720,60 @@ def svdq_linear(x: torch.Tensor, w: PreparedWeights, y: Optional[torch.Tensor] =
     qact, asc, lr = quantize_act(x, w.smooth, w.proj_down, stream=stream)
     return w4a4_linear(qact, asc, lr, w.qweight, w.wscales_tiled, w.wcscales, w.wtscale,
                        w.proj_up, w.bias, y=y, stream=stream, proj_up_folded=w.proj_up_folded)
+
+
+class DitBlock:
+    """One transformer block: its five linears (PreparedWeights) and the bf16
+    vectors of its norms.
+
+    qkv [C -> 3 heads head_dim] (q, then k, then v, head by head), out, w1, w3,
+    w2; attn_pre, attn_post, ffn_pre, ffn_post: RMS norm weights [C] in front
+    of and behind the attention and the feed-forward; q_norm, k_norm: per-head
+    RMS norm weights [head_dim]."""
+
+    def __init__(self, qkv: PreparedWeights, out: PreparedWeights, w1: PreparedWeights,
+                 w3: PreparedWeights, w2: PreparedWeights, *, heads: int, attn_pre, attn_post,
+                 ffn_pre, ffn_post, q_norm, k_norm, eps: float = 1e-6):
+        C, F = qkv.K, w1.N
+        if heads < 1 or qkv.N % (3 * heads) or out.K * 3 != qkv.N:
+            raise ValueError(f"qkv makes {qkv.N} and out takes {out.K}: not 3 x {heads} heads")
+        if (out.N, w1.K, w3.K, w3.N, w2.K, w2.N) != (C, C, C, F, F, C):
+            raise ValueError(f"the linears do not fit a width of {C} and a feed-forward of {F}")
+        self.qkv, self.out, self.w1, self.w3, self.w2 = qkv, out, w1, w3, w2
+        self.heads, self.head_dim = heads, qkv.N // (3 * heads)
+        self.attn_pre, self.attn_post = attn_pre, attn_post
+        self.ffn_pre, self.ffn_post = ffn_pre, ffn_post
+        self.q_norm, self.k_norm = q_norm, k_norm
+        self.eps = eps
+
+
+def dit_block(x: torch.Tensor, w: DitBlock, modulation, positions: torch.Tensor, plan: RopePlan,
+              cu_seqlens: Optional[torch.Tensor] = None, causal: bool = False) -> torch.Tensor:
+    """One block on x [T, C] bf16 on the current stream -> the new x:
+
+        x = x + tanh(gate_attn) * norm(out(attention(rope(qkv(norm(x) (1 + scale_attn))))))
+        x = x + tanh(gate_ffn) * norm(w2(silu(w1 n) * w3 n)),  n = norm(x) (1 + scale_ffn)
+
+    modulation: (scale_attn, gate_attn, scale_ffn, gate_ffn), each [n_seqs, C];
+    rows by cu_seqlens (None: one sequence).  Rows in no sequence come back
+    undefined."""
+    scale_attn, gate_attn, scale_ffn, gate_ffn = modulation
+    T, H, D, eps = x.shape[0], w.heads, w.head_dim, w.eps
+    _, n = norm_gate_residual(x, scale=scale_attn, pre_weight=w.attn_pre, eps=eps,
+                              cu_seqlens=cu_seqlens)
+    qkv = svdq_linear(n, w.qkv).view(T, 3 * H, D)
+    q, k, v = qkv[:, :H], qkv[:, H:2 * H], qkv[:, 2 * H:]
+    rope_qk(q, k, positions, plan, w.q_norm, w.k_norm, eps, q_out=q, k_out=k)
+    a = attention(q, k, v, cu_seqlens, causal)
+    y = svdq_linear(a.view(T, H * D), w.out)
+    x, n = norm_gate_residual(x, y, gate=gate_attn, gate_tanh=True, post="rms",
+                              post_weight=w.attn_post, pre_weight=w.ffn_pre, scale=scale_ffn,
+                              eps=eps, cu_seqlens=cu_seqlens)
+    w2 = w.w2
+    qact, asc, lr = silu_mul_quantize_act(svdq_linear(n, w.w1), svdq_linear(n, w.w3), w2.smooth,
+                                          w2.proj_down)
+    y = w4a4_linear(qact, asc, lr, w2.qweight, w2.wscales_tiled, w2.wcscales, w2.wtscale,
+                    w2.proj_up, w2.bias, proj_up_folded=w2.proj_up_folded)
+    x, _ = norm_gate_residual(x, y, gate=gate_ffn, gate_tanh=True, post="rms",
+                              post_weight=w.ffn_post, pre=None, eps=eps, cu_seqlens=cu_seqlens)
+    return x
