@@ -299,9 +299,11 @@ int svdq_quantize_weights_noalloc(const uint16_t* W, const uint16_t* smooth, con
  *   [0, T]; NULL (with n_seqs = 1): one sequence of all T rows.  Sequences
  *   may be empty.  Rows in no sequence are not read for a result and their
  *   outputs stay as they were.  The array is not checked on the host; the
- *   kernels stay inside the tensors whatever it holds.
- * - Strides are in elements, multiples of 8; 16-bit tensors are 16-byte
- *   aligned.  The stride of a dimension of size one is not used.
+ *   kernels stay inside the tensors whatever it holds (an offset below an
+ *   earlier one is then taken as that one, by svdq_attention).
+ * - Strides are in elements, positive multiples of 8, at least the piece
+ *   they step over; 16-bit tensors are 16-byte aligned.  The stride of a
+ *   dimension of size one is not used.
  * - T = 0 returns SVDQ_OK and enqueues nothing.
  * - The library keeps nothing between calls: calls on several streams, and
  *   captured calls, share nothing but the memory they are given.
@@ -392,8 +394,8 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
  *                 on the same device; with and without workspace they may
  *                 differ in the last bits of the fp32 sums.  Calls that may
  *                 overlap on the GPU need workspaces of their own.
- * Limits: Hq % Hk == 0, D % 8 == 0, D <= 128 (else SVDQ_ERR_SHAPE /
- * SVDQ_ERR_UNSUPPORTED). */
+ * Limits: Hq % Hk == 0 (else SVDQ_ERR_SHAPE), D % 8 == 0, D <= 128, T < 2^30,
+ * (T / 256 + n_seqs) * Hq < 2^30 (else SVDQ_ERR_UNSUPPORTED). */
 size_t svdq_attention_workspace_bytes(int T, int n_seqs, int Hq, int D, int causal);
 
 int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h,

@@ -143,9 +143,10 @@ struct Item {
   }
 };
 
-// Walks a block's work: one warp does and tells the others.  Offsets are
-// clamped to [0, T] and to an increasing order, so that no entry of cu can
-// lead outside the tensors.
+// Walks a block's work: one warp does and tells the others.  Sequence s is
+// [e_s, e_s+1), e_s the largest of cu[0 .. s] clamped to [0, T]: offsets that
+// do not fall are taken as they are, and whatever cu holds the sequences lie
+// inside the tensors, do not meet, and have at most T rows together.
 //
 // Whole items: block b takes the items b, b + blocks, ... of all sequences
 // (causal: longest first within a sequence).  Split: the items of all
@@ -158,6 +159,7 @@ struct Items {
   int begin_ = 0, len_ = 0;       //   its rows,
   int incl_ = 0, size_ = 0;       //   places up to its end (within the group), its places
   int base = 0, next_base = 0;    // places in front of the group, of the next
+  int front = 0;                  // where the next group's rows begin, at least
   int at = 0, end = 0;
 
   // Of a sequence: items, or places of one head's items.
@@ -173,11 +175,18 @@ struct Items {
     s0 += 32;
     base = next_base;
     const int lane = threadIdx.x & 31, s = s0 + lane;
-    begin_ = len_ = 0;
-    if (s < p.S) {
-      begin_ = p.cu ? min(max(p.cu[s], 0), p.T) : 0;
-      len_ = (p.cu ? min(max(p.cu[s + 1], begin_), p.T) : p.T) - begin_;
+    begin_ = 0;
+    int stop = s < p.S && !p.cu ? p.T : 0;
+    if (s < p.S && p.cu) {
+      begin_ = min(max(p.cu[s], 0), p.T);
+      stop = min(max(p.cu[s + 1], 0), p.T);
     }
+    begin_ = max(begin_, front);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) begin_ = max(begin_, __shfl_up_sync(0xFFFFFFFFu, begin_, o));
+    stop = max(stop, begin_);
+    front = __shfl_sync(0xFFFFFFFFu, stop, 31);
+    len_ = stop - begin_;
     incl_ = size_ = size(p, len_);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -220,7 +229,7 @@ struct Items {
   // near (two partial results less).
   __device__ __forceinline__ int edge(const Params& p, int w, int total, int run) {
     if (w >= total) return total;
-    if (p.S > 32) s0 = -32, next_base = 0;   // from the first group on again
+    if (p.S > 32) s0 = -32, next_base = front = 0;   // from the first group on again
     Item it;
     const int r = locate(p, w, it), n = it.all_tiles(p.causal) + 1;
     const int near = 1 + max(1, run / 16);
@@ -236,7 +245,7 @@ struct Items {
     const int64_t w = static_cast<int64_t>(blockIdx.x) * run;
     end = edge(p, static_cast<int>(min(w + run, static_cast<int64_t>(total))), total, run);
     at = edge(p, static_cast<int>(min(w, static_cast<int64_t>(total))), total, run);
-    if (p.S > 32) s0 = -32, next_base = 0;
+    if (p.S > 32) s0 = -32, next_base = front = 0;
   }
   __device__ __forceinline__ bool get(const Params& p, Item& it) {
     if (SPLIT) {

@@ -1047,6 +1047,12 @@ bool may_meet(const Extent& a, const Extent& b) {
   return true;
 }
 
+// Whether pieces of one strided output share a byte.
+bool meets_itself(const Extent& a) {
+  return a.outer > 1 && a.inner > 1 && (a.inner - 1) * a.sh + a.bytes > a.st &&
+         (a.outer - 1) * a.st + a.bytes > a.sh;
+}
+
 // An output may be exactly an input (each element is read before it is
 // written, by the same thread), or else has to lie apart from it.
 bool bad_overlap(const Extent& out, const Extent& in) { return !same(out, in) && may_meet(out, in); }
@@ -1306,8 +1312,8 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
   const Extent eqo = extent(q_out, T, qo_stride_t, Hq, qo_stride_h, D);
   const Extent eko = extent(k_out, T, ko_stride_t, Hk, ko_stride_h, D);
   const Extent epos = {reinterpret_cast<uintptr_t>(positions), T, 4 * ld_pos, 1, 4, 4 * n_axes};
-  if ((has_q && (bad_overlap(eqo, eq) || may_meet(eqo, epos))) ||
-      (has_k && (bad_overlap(eko, ek) || may_meet(eko, epos))) ||
+  if ((has_q && (meets_itself(eqo) || bad_overlap(eqo, eq) || may_meet(eqo, epos))) ||
+      (has_k && (meets_itself(eko) || bad_overlap(eko, ek) || may_meet(eko, epos))) ||
       (has_q && has_k && (may_meet(eqo, ek) || may_meet(eko, eq) || may_meet(eqo, eko))))
     return SVDQ_ERR_INVALID_ARG;
   const Extent ws[] = {extent(q_weight, 1, D, 1, D, D), extent(k_weight, 1, D, 1, D, D)};
@@ -1383,7 +1389,8 @@ int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_s
   if (T < 0 || Hq < 1 || Hk < 1 || Hq % Hk || D < 1 || n_seqs < 1 || (!cu_seqlens && n_seqs != 1))
     return SVDQ_ERR_SHAPE;
   if (D % 8 || D > svdq::ka::MAX_D ||
-      (static_cast<int64_t>(T) / svdq::ka::ITEM_ROWS + 1) * Hq > INT_MAX)
+      T > INT_MAX / 2 ||
+      (static_cast<int64_t>(T) / svdq::ka::ITEM_ROWS + n_seqs) * Hq > INT_MAX / 2)
     return SVDQ_ERR_UNSUPPORTED;
   if (T == 0) return SVDQ_OK;
   if (!q || !k || !v || !out) return SVDQ_ERR_INVALID_ARG;
@@ -1411,7 +1418,8 @@ int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_s
   const Extent ek = extent(k, T, k_stride_t, Hk, k_stride_h, D);
   const Extent ev = extent(v, T, v_stride_t, Hk, v_stride_h, D);
   const Extent eo = extent(out, T, o_stride_t, Hq, o_stride_h, D);
-  if (may_meet(eo, eq) || may_meet(eo, ek) || may_meet(eo, ev)) return SVDQ_ERR_INVALID_ARG;
+  if (meets_itself(eo) || may_meet(eo, eq) || may_meet(eo, ek) || may_meet(eo, ev))
+    return SVDQ_ERR_INVALID_ARG;
   if (workspace) {
     const Extent ew = {reinterpret_cast<uintptr_t>(workspace), 1, 0, 1, 0,
                        static_cast<int64_t>(workspace_bytes)};

@@ -100,6 +100,7 @@ ROPE_BAD = [
     ("INVALID_ARG", dict(qo=1 * MB + 256, qost=192)),    # over k
     ("INVALID_ARG", dict(ko=4 * MB)),                    # over q_out
     ("INVALID_ARG", dict(qo=3 * MB)),                    # over the positions
+    ("INVALID_ARG", dict(qost=64)),                      # its own heads meet
     ("SHAPE", dict(axes=(16, 24, 32))), ("SHAPE", dict(axes=(15, 24))), ("SHAPE", dict(axes=(0, 24))),
     ("SHAPE", dict(T=-1)), ("SHAPE", dict(Hq=-1)), ("SHAPE", dict(D=0)), ("SHAPE", dict(ldp=2)),
     ("SHAPE", dict(qst=32)), ("SHAPE", dict(qosh=32)),
@@ -159,7 +160,9 @@ ATTN_BAD = [
     ("SHAPE", dict(D=0)), ("SHAPE", dict(S=0)), ("SHAPE", dict(S=2)), ("SHAPE", dict(qst=32)),
     ("SHAPE", dict(ksh=56)), ("SHAPE", dict(vst=-512)),
     ("UNSUPPORTED", dict(D=60)), ("UNSUPPORTED", dict(D=136, qsh=136, ksh=136, vsh=136, osh=136)),
-    ("UNSUPPORTED", dict(Hq=1 << 20, Hk=1 << 20, T=1 << 20)),
+    ("UNSUPPORTED", dict(Hq=1 << 20, Hk=1 << 20, T=1 << 20)), ("UNSUPPORTED", dict(T=1 << 30)),
+    ("UNSUPPORTED", dict(cu=MB, S=1 << 29)),
+    ("INVALID_ARG", dict(ost=64, osh=64)), ("INVALID_ARG", dict(ost=128, osh=64)),     # out's own rows meet
     ("UNSUPPORTED", dict(qst=1 << 39)),
     ("ALIGNMENT", dict(k=MB + 520)), ("ALIGNMENT", dict(vst=516)), ("ALIGNMENT", dict(osh=68)),
     ("ALIGNMENT", dict(cu=MB + 1)), ("ALIGNMENT", dict(ws=5 * MB + 8, ws_bytes=1 << 30)),
@@ -203,6 +206,87 @@ def test_binding_refuses_host_tensors_and_wrong_types(svdq):
         svdq.attention(q, q, q)
 
 
+# ---- the divided walk: places of a line, cut into runs ----------------------------
+
+def place_items(lens, Hq, causal):
+    """(first place, item) of every item in order; an item takes a place more
+    than its key tiles."""
+    at, begin, out = 0, 0, []
+    for n in lens:
+        for head in range(Hq):
+            for q0 in range(0, n, ITEM):
+                k = max(tiles(n, q0, 0, causal), tiles(n, q0, 1, causal))
+                out.append((at, begin, n, q0, head, k))
+                at += k + 1
+        begin += n
+    return out, at
+
+
+def causal_index(r2):
+    import math
+    i = int(math.sqrt(r2 + 1.0)) - 1
+    while i > 0 and i * (i + 2) > r2:
+        i -= 1
+    while (i + 1) * (i + 3) <= r2:
+        i += 1
+    return i
+
+
+def locate(lens, Hq, causal, w):
+    """The kernel's closed form: (begin, n, q0, head), place in the item."""
+    begin = 0
+    for n in lens:
+        nt, nk = (n + ITEM - 1) // ITEM, (n + ROWS - 1) // ROWS
+        per = nt * (nt + 2) - (2 * nt - nk) if causal else nt * (nk + 1)
+        if w < per * Hq:
+            head, r2 = divmod(w, per)
+            if causal:
+                i = causal_index(r2)
+                return (begin, n, i * ITEM, head), r2 - i * (i + 2)
+            return (begin, n, r2 // (nk + 1) * ITEM, head), r2 % (nk + 1)
+        w -= per * Hq
+        begin += n
+    return None, -1
+
+
+def run_edge(lens, Hq, causal, w, total, run):
+    if w >= total:
+        return total
+    (begin, n, q0, head), r = locate(lens, Hq, causal, w)
+    k = max(tiles(n, q0, 0, causal), tiles(n, q0, 1, causal)) + 1
+    near = 1 + max(1, run // 16)
+    return w - r if r <= near else w + k - r if k - r < near else w
+
+
+@pytest.mark.parametrize("lens,Hq", [([16384], 1), ([8192], 2), ([2600], 1), ([5000, 1, 0, 4000], 3), ([700], 2)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_divided_runs_cover_every_key_tile_once(lens, Hq, causal):
+    line, total = place_items(lens, Hq, causal)
+    for at, begin, n, q0, head, k in line:
+        for r in range(k + 1):
+            assert locate(lens, Hq, causal, at + r) == ((begin, n, q0, head), r)
+    G = 148
+    run = max(6, (total + G - 1) // G)
+    seen, ends = set(), []
+    for b in range(G):
+        at = run_edge(lens, Hq, causal, min(b * run, total), total, run)
+        end = run_edge(lens, Hq, causal, min((b + 1) * run, total), total, run)
+        first = True
+        while at < end:
+            (begin, n, q0, head), r = locate(lens, Hq, causal, at)
+            k = max(tiles(n, q0, 0, causal), tiles(n, q0, 1, causal))
+            ka, kb = max(0, r - 1), min(k, end - at + r - 1)
+            assert 0 <= ka < kb <= k
+            assert ka == 0 or first          # only a run's first item may have begun in front of it
+            assert kb == k or at + 1 + kb - r >= end
+            for j in range(ka, kb):
+                assert (begin, q0, head, j) not in seen
+                seen.add((begin, q0, head, j))
+            at += 1 + kb - r
+            first = False
+    assert len(seen) == sum(k for *_, k in line)
+
+
 # ---- the attention kernel's work items -------------------------------------------
 
 ROWS, ITEM = 128, 256
@@ -217,7 +301,7 @@ def items(cu, T, Hq, causal):
         while s0 < S:
             incl, rows = 0, []
             for s in range(s0, min(s0 + 32, S)):
-                begin = min(max(cu[s], 0), T)
+                begin = min(max(max(cu[:s + 1]), 0), T)
                 n = min(max(cu[s + 1], begin), T) - begin
                 count = (n + ITEM - 1) // ITEM * Hq
                 incl += count
@@ -273,9 +357,13 @@ def test_items_cover_every_row_and_head_once(lens, causal):
     assert len(seen) == T * Hq
 
 
-@pytest.mark.parametrize("cu", [[5, 2, 900, 300], [-7, 10, 2000, 2 ** 31 - 1], [-2 ** 31, 2 ** 31 - 1], [3, 3, 3]])
+@pytest.mark.parametrize("cu", [[5, 2, 900, 300], [-7, 10, 2000, 2 ** 31 - 1], [-2 ** 31, 2 ** 31 - 1], [3, 3, 3],
+                                [0, 777] * 40])
 def test_items_of_bad_offsets_stay_inside(cu):
     T = 777
+    # no row twice, so at most T rows together
+    seen = [(b + r, h) for b, n, q0, h in items(cu, T, 2, False) for r in range(q0, min(n, q0 + ITEM))]
+    assert len(seen) == len(set(seen)) <= 2 * T
     for begin, n, q0, head in items(cu, T, 2, True):
         assert 0 <= begin and begin + n <= T and 0 <= q0 < n and 0 <= head < 2
 

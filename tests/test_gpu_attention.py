@@ -242,7 +242,7 @@ def test_bad_offsets_stay_inside():
     T = 300
     q, k, v = make(T, 2, 1, 64, seed=15)
     wide = torch.full((3 * T, 2, 64), 7.0, dtype=BF, device=DEV)
-    for cu in ([-5, 100, 2 ** 31 - 1], [200, 50, 300], [-2 ** 31, -1, 1000], [301, 400, 500]):
+    for cu in ([-5, 100, 2 ** 31 - 1], [200, 50, 300], [-2 ** 31, -1, 1000], [301, 400, 500], [0, 300] * 40):
         for causal in (False, True):
             H.svdq().attention(q, k, v, torch.tensor(cu, dtype=torch.int32, device=DEV), causal, out=wide[T:2 * T])
             H.svdq().check_device_error()
@@ -373,3 +373,31 @@ def test_divided_items_keep_bad_keys_and_values_apart(bad):
         k2[at, 0, 9] = float("nan")
         got = H.svdq().attention(q, k2, v, causal=True)
         assert torch.equal(got[:at], clean[:at]) and torch.isnan(got[at:]).all()
+
+
+@pytest.mark.parametrize("what", ["norm", "rope", "attention", "divided"])
+def test_first_call_of_a_process_may_be_captured(what):
+    """A fresh process whose first call of the operator is under capture."""
+    import os
+    import subprocess
+    import sys
+    code = """
+import torch
+from nvfp4_w4a4_quantized_smooth_b200 import svdq as s
+T = 4000
+x = torch.randn(T, 256, device="cuda").bfloat16()
+q = x.view(T, 2, 128)
+pos = torch.zeros(T, 3, dtype=torch.int32, device="cuda")
+calls = dict(norm=lambda: s.norm_gate_residual(x, x)[0], rope=lambda: s.rope_qk(q, None, pos, s.RopePlan((32, 48, 48), 256.0, 128))[0],
+             attention=lambda: s.attention(q[:300], q[:300], q[:300]), divided=lambda: s.attention(q, q, q))
+f = calls["%s"]
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = f()
+g.replay()
+s.check_device_error()
+assert torch.equal(got, f())
+""" % what
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
