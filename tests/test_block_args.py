@@ -293,32 +293,42 @@ ROWS, ITEM = 128, 256
 
 
 def items(cu, T, Hq, causal):
-    """The walk of the kernel: groups of 32 sequences, items in order."""
-    S = len(cu) - 1
-    w, s0, base = 0, 0, 0
-    while True:
-        found = False
-        while s0 < S:
-            incl, rows = 0, []
-            for s in range(s0, min(s0 + 32, S)):
-                begin = min(max(max(cu[:s + 1]), 0), T)
-                n = min(max(cu[s + 1], begin), T) - begin
-                count = (n + ITEM - 1) // ITEM * Hq
-                incl += count
-                rows.append((incl, count, begin, n))
-            hit = next((r for r in rows if base + r[0] > w), None)
-            if hit is not None:
-                incl, count, begin, n = hit
-                r, nt = w - base - (incl - count), (n + ITEM - 1) // ITEM
-                head, tile = (r % Hq, nt - 1 - r // Hq) if causal else (r // nt, r % nt)
-                yield begin, n, tile * ITEM, head
-                found = True
-                break
-            base += incl
-            s0 += 32
-        if not found:
-            return
-        w += 1
+    """The line of items that the kernel deals out: groups of 32 sequences;
+    causal: item i of every sequence that has one, then i - 1; full: longest
+    sequence first."""
+    S, front = len(cu) - 1, 0
+    for s0 in range(0, S, 32):
+        seqs = []
+        for s in range(s0, min(s0 + 32, S)):
+            begin = max(min(max(cu[s], 0), T), front)
+            front = max(min(max(cu[s + 1], 0), T), begin)
+            seqs.append((begin, front - begin))
+        if causal:
+            for i in range(max((n + ITEM - 1) // ITEM for _, n in seqs) - 1, -1, -1):
+                yield from ((b, n, i * ITEM, h) for b, n in seqs if n > i * ITEM for h in range(Hq))
+        else:
+            for b, n in sorted(seqs, key=lambda x: -x[1]):
+                yield from ((b, n, q0, h) for h in range(Hq) for q0 in range(0, n, ITEM))
+
+
+def dealt(line, blocks):
+    """The items of each block: rounds, every other one turned."""
+    out = [[] for _ in range(blocks)]
+    for k, at in enumerate(range(0, len(line), blocks)):
+        for b in range(blocks):
+            w = at + (blocks - 1 - b if k % 2 else b)
+            if w < len(line):
+                out[b].append(line[w])
+    return out
+
+
+@pytest.mark.parametrize("blocks", [1, 7, 148])
+def test_items_are_dealt_once_and_evenly(blocks):
+    line = list(items([0, 5000, 5100, 9000], 9000, 8, True))
+    got = dealt(line, blocks)
+    assert sorted(x for b in got for x in b) == sorted(line)
+    load = [sum(max(tiles(n, q0, 0, True), tiles(n, q0, 1, True)) for _, n, q0, _ in b) for b in got]
+    assert max(load) <= 1.25 * sum(load) / blocks + 2
 
 
 def tiles(n, q0, s, causal):
