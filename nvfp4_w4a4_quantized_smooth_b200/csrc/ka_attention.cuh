@@ -57,9 +57,9 @@ constexpr int MIN_RUN = 6;               // places of a block's run, at least (s
 constexpr int P_STEPS = 6;              // 16-key steps of P that are handed over first
 constexpr float RESCALE_LOG2 = 8.f;
 // Registers per thread of the softmax warps and of the others: all that the
-// block has (384 x 168).  The softmax loop is slower with fewer (208: 275 us
-// against 236 at 4352 x 30 heads), the others spill with fewer (224 / 56: 247).
-constexpr int SOFTMAX_REGS = 216, OTHER_REGS = 72;
+// block has (384 x 168).  At 4352 x 30 heads 237 us, 250 with 216 / 72 or
+// 224 / 56.
+constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
 
 // NB: 64-element boxes per row (1: D <= 64, 2: D <= 128).
 template <int NB>
@@ -337,6 +337,41 @@ __device__ __forceinline__ bool is_nonfinite16(uint32_t e) {
   return (e & m) == m;
 }
 
+// The larger of a's halves and the magnitudes of b's, NaN if one is NaN.
+template <bool BF16>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  b &= 0x7FFF7FFFu;
+  if (BF16)
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+
+// Replaces the non-finite values of the first `valid` rows of a tile by zero
+// and notes their keys (it hardly ever runs).
+template <bool BF16, int NB>
+__device__ __forceinline__ void clean_tile(uint32_t tile, int valid, uint32_t* notes) {
+  for (int b = 0; b < NB; ++b) {
+    for (int c = threadIdx.x & 31; c < 8 * valid; c += 32) {
+      const uint32_t at = tile + b * BOX_BYTES + 16 * c;
+      uint32_t x[4];
+      bool bad = false;
+      ld_shared_v4(at, x[0], x[1], x[2], x[3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (is_nonfinite16<BF16>(x[i])) x[i] &= 0xFFFF0000u, bad = true;
+        if (is_nonfinite16<BF16>(x[i] >> 16)) x[i] &= 0x0000FFFFu, bad = true;
+      }
+      if (bad) {
+        st_shared_v4(at, x[0], x[1], x[2], x[3]);
+        atomicOr(notes + (c >> 8), 1u << ((c >> 3) & 31));
+      }
+    }
+  }
+}
+
 template <bool BF16, int NB, bool SPLIT>
 __global__ void __launch_bounds__(NUM_THREADS, 1)
     attention_kernel(const __grid_constant__ CUtensorMap tm_q,
@@ -494,11 +529,14 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
     } else if (warp != GUARD_WARP) {
       // ------------------------------------------------------------ MMA --
       // A warp per slot; they take turns at the tensor core, a slot's P V and
-      // next Q K^T at a time, which keeps the slots half a period apart (left
-      // alone they fall into step and wait for the same unit at the same
-      // time: 365 us against 285 at 4352 x 30 heads).  It stays together (one lane issues), so that
-      // descriptors are uniform and an MMA costs an addition or two to issue:
-      // the tensor core takes 64 cycles for one.
+      // next Q K^T at a time, the next turn beginning when these are done.
+      // That keeps the slots half a period apart: left alone they fall into
+      // step and want the same unit at the same time (4352 x 30 heads: 365
+      // us), and with the turn handed on earlier one slot's last weights are
+      // taken beside the other's first ones (278 us, against 252).
+      // The warp stays together (one lane issues), so that descriptors are
+      // uniform and an MMA costs an addition or two to issue: the tensor core
+      // takes 64 cycles for one.
       const int s = warp - MMA_WARP;
       const uint32_t leader = elect_one();
       const uint32_t dn = (p.D + 15) / 16 * 16;   // columns of O, and k of Q K^T
@@ -529,8 +567,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
         const int last = it.key_tiles() - 1 - it.ka;    // the sequence's last
         const int last_steps = (it.len % ROWS + ROWS - 1) % ROWS / 16 + 1;   // 16-key steps of that one
         const int guard_from = it.guard_from(p.causal) - it.ka;
-        // S of tile j from stage `at`; the other slot's turn begins while the
-        // last products are issued.
+        // S of tile j from stage `at`; with `pass` the other slot's turn begins
+        // when it is done.
         auto qk = [&](int j, uint32_t at, bool pass) {
           if (j < mine) {
             const uint32_t keys = j == last ? 16 * last_steps : ROWS;
@@ -540,9 +578,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int c = 0; c < 4 * NB; ++c) {
               const uint64_t off = ((c >> 2) * BOX_BYTES + 32 * (c & 3)) / 16;
               if (c < dk) mma_f16_by(leader, tm_s, desc_q + off, dkk + off, id, c != 0);
-              if (c == 2 * NB - 1 && pass && leader) mbar_arrive(turn_bar + 8 * (s ^ 1));
             }
             tc_commit_by(leader, b_s);
+            if (pass) tc_commit_by(leader, turn_bar + 8 * (s ^ 1));
           } else if (pass && leader) {
             mbar_arrive(turn_bar + 8 * (s ^ 1));
           }
@@ -636,27 +674,22 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int c = 8 * valid + lane; c < 8 * stop; c += 32)
               st_shared_v4(tile + b * BOX_BYTES + 16 * c, 0u, 0u, 0u, 0u);
           if (p.causal) {
+            // First only whether there is a non-finite value at all: the
+            // largest magnitude of each lane's words, NaN if there is one.
+            uint32_t top = 0;
             for (int b = 0; b < NB; ++b) {
+              const uint32_t box = tile + b * BOX_BYTES;
 #pragma unroll 8
               for (int c = lane; c < 8 * valid; c += 32) {
-                const uint32_t at = tile + b * BOX_BYTES + 16 * c;
                 uint32_t x[4];
-                ld_shared_v4(at, x[0], x[1], x[2], x[3]);
-                constexpr uint32_t m = BF16 ? 0x7F807F80u : 0x7C007C00u;
-                constexpr uint32_t one = BF16 ? 0x00800080u : 0x04000400u;
-                uint32_t bad = 0;
+                ld_shared_v4(box + 16 * c, x[0], x[1], x[2], x[3]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) bad |= (x[i] & m) + one;
-                if ((bad & 0x80008000u) != 0u) {
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    if (is_nonfinite16<BF16>(x[i])) x[i] &= 0xFFFF0000u;
-                    if (is_nonfinite16<BF16>(x[i] >> 16)) x[i] &= 0x0000FFFFu;
-                  }
-                  st_shared_v4(at, x[0], x[1], x[2], x[3]);
-                  atomicOr(fj + (c >> 8), 1u << ((c >> 3) & 31));
-                }
+                for (int i = 0; i < 4; ++i) top = max_abs2<BF16>(top, x[i]);
               }
+            }
+            const bool bad = is_nonfinite16<BF16>(top) || is_nonfinite16<BF16>(top >> 16);
+            if (__any_sync(0xFFFFFFFFu, bad)) {
+              clean_tile<BF16, NB>(tile, valid, fj);
             }
           }
           fence_proxy_async_smem();
