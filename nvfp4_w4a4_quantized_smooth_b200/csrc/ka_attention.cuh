@@ -19,7 +19,7 @@
 // more than 2^8 over its reference: until then the exponentials stay below
 // 2^8, which neither the fp32 sums nor the 16-bit P lose digits over (P's
 // relative rounding is the same at every exponent, fp16's range is 65504).
-// P is rounded to the input type for the tensor core (half a step, 2^-9 of
+// P is rounded to the input type for the tensor core (half a step, 2^-8 of
 // each weight for bf16); the sum is over the unrounded fp32 weights.
 //
 // Keys that a row does not attend are replaced by -inf after the product, by
@@ -30,6 +30,17 @@
 // rows behind the end (only up to the next multiple of 16; the product stops
 // there) and, when causal, replaces non-finite values by zero and notes their
 // keys; the epilogue adds a noted value back into the rows that do attend it.
+//
+// Bound: per key tile and 256 rows the tensor core has 2048 cycles of products
+// (D = 128) and the special function units 2048 cycles of exponentials; a
+// slot's tile is a chain of both (about 1350 cycles from S to P, 1500 from P
+// to the next S), so two slots in turns need about 2800.  At 4352 rows x 30
+// heads of 128: 240 us in short runs (1210 TFLOP/s, 73% of what a cuBLAS
+// product of 8192^3 reaches), 285 us in runs of a second, where the GPU is at
+// its power limit and lowers the clock (cuBLAS then: 1403 TFLOP/s).  What was
+// tried against that: exponentials by a polynomial on the FMA units (1/8 of
+// them: 307 us, more: slower still), handing over half of P first (286 against
+// 250), five stages of the ring (1083 us against 974 at four times the rows).
 #pragma once
 
 #include <climits>

@@ -17,7 +17,10 @@
 // by bulk copies into a ring in shared memory, four rows ahead, which takes
 // no registers and no load instructions; the statistics of a row's branch
 // are summed together with those of the previous row's h, so that a row
-// costs one block barrier.
+// costs one block barrier.  4352 rows x 3840 (134 MB): 26.3 us, 5.1 TB/s; 17408
+// rows with layer norm (two barriers a row): 95 us, 5.6 TB/s, 87% of a plain
+// copy's rate.  Loads one row ahead into registers took 29.6 us, a warp per row
+// (no barrier, but 255 registers and spills) 38.
 #pragma once
 
 #include <cstdint>
