@@ -337,7 +337,7 @@ int svdq_quantize_weights_noalloc(const uint16_t* W, const uint16_t* smooth, con
  *   h [T, ldh]    out;  n [T, ldn] out, or NULL (then pre, scale and shift
  *                 none): only h.
  * h and n may each be exactly x or y (same address and stride).
- * Limits: C % 8 == 0, C <= 8192 (else SVDQ_ERR_UNSUPPORTED). */
+ * Limits: C % 8 == 0, C <= 8192, T < 2^30 (else SVDQ_ERR_UNSUPPORTED). */
 int svdq_norm_gate_residual(int dtype, const uint16_t* x, int64_t ldx, const uint16_t* y,
                             int64_t ldy, int T, int C, const int32_t* cu_seqlens, int n_seqs,
                             int post, const uint16_t* post_weight, int gate_kind,
@@ -347,8 +347,8 @@ int svdq_norm_gate_residual(int dtype, const uint16_t* x, int64_t ldx, const uin
                             int64_t ldh, uint16_t* n, int64_t ldn, void* stream);
 
 /* Frequencies of svdq_rope_qk: turns[p] = theta^(-2 i / axes[a]) / (2 pi) for
- * pair p, the i-th of axis a (axes one behind the other).  axes and turns are
- * HOST arrays, turns [sum(axes) / 2]; no device work.  A caller with
+ * pair p, the i-th of axis a (axes one behind the other); theta >= 1.  axes and
+ * turns are HOST arrays, turns [sum(axes) / 2]; no device work.  A caller with
  * frequencies of its own fills turns itself. */
 int svdq_rope_turns(const int* axes, int n_axes, double theta, double* turns);
 
@@ -362,13 +362,14 @@ int svdq_rope_turns(const int* axes, int n_axes, double theta, double* turns);
  *   q [T, Hq, D], k [T, Hk, D]   by strides (token, head); either may be
  *                 absent (heads 0, pointers NULL).
  *   positions     [T, ld_pos] int32, device, n_axes columns used, any value
- *                 (angles are taken in 64 bits).
+ *                 (angles are taken in 64 bits: with turns of at most
+ *                 1 / (2 pi) the error stays below 2^-22 turns).
  *   axes, turns   HOST arrays [n_axes] (even widths) and [R / 2], read during
  *                 the call.
  *   q_weight, k_weight   [D] or NULL: no norm for that tensor.
  *   q_out, k_out  out, same shapes; each may be exactly its input.
- * Limits: n_axes <= 4, D % 8 == 0, D <= 256, R <= D, and R % 8 == 0 without
- * interleaving (else SVDQ_ERR_UNSUPPORTED). */
+ * Limits: n_axes <= 4, D % 8 == 0, D <= 256, R <= D, Hq + Hk <= 2^16, T < 2^30,
+ * and R % 8 == 0 without interleaving (else SVDQ_ERR_UNSUPPORTED). */
 int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_stride_h, int Hq,
                  const uint16_t* k, int64_t k_stride_t, int64_t k_stride_h, int Hk, int T, int D,
                  const int32_t* positions, int64_t ld_pos, const int* axes, int n_axes,
@@ -384,7 +385,7 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
  * rounded to the tensors' type for the product with v.  Keys and values that
  * a row does not attend, whatever they hold (inf, NaN), do not reach it.
  *   q [T, Hq, D], k, v [T, Hk, D], out [T, Hq, D]  by strides (token, head).
- *   scale         finite and positive (usually 1 / sqrt(D)).
+ *   scale         positive, scale * log2(e) finite (usually 1 / sqrt(D)).
  *   workspace     NULL, or at least svdq_attention_workspace_bytes(...) bytes
  *                 (for this call's arguments, on this device; 0: none is of
  *                 use), 16-byte aligned, overwritten.  With it, where rows

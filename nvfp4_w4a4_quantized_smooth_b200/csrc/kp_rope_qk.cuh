@@ -17,7 +17,7 @@
 // with the norm's weights into sixteen registers for all heads of a unit.
 // Angles are taken in turns in 64 bits and reduced there before the 32-bit
 // sine and cosine, so a position of any int32 value keeps an angle error
-// below 2^-23 turns.  4352 tokens x 60 heads of 128 (134 MB): 28.9 us, 4.6 TB/s;
+// below 2^-22 turns.  4352 tokens x 60 heads of 128 (134 MB): 28.9 us, 4.6 TB/s;
 // 9973 tokens x 40 heads in halves (204 MB): 40.9 us, 5.0 TB/s.  Issue slots
 // are 60% taken; a block per few tokens with a barrier for the angles took
 // 32.6 us, one with the whole block on a shared ring 34.1 (warps waiting for

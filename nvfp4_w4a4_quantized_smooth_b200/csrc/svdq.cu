@@ -1029,6 +1029,10 @@ Extent extent(const void* p, int64_t outer, int64_t st, int64_t inner, int64_t s
   return {reinterpret_cast<uintptr_t>(p), outer, 2 * st, inner, 2 * sh, 2 * cols};
 }
 
+Extent offsets(const int32_t* cu, int n_seqs) {
+  return {reinterpret_cast<uintptr_t>(cu), 1, 0, 1, 0, 4 * (static_cast<int64_t>(n_seqs) + 1)};
+}
+
 bool same(const Extent& a, const Extent& b) {
   return a.base == b.base && (a.st == b.st || a.outer == 1) && (a.sh == b.sh || a.inner == 1);
 }
@@ -1190,8 +1194,11 @@ int svdq_norm_gate_residual(int dtype, const uint16_t* x, int64_t ldx, const uin
   if ((gate_kind != SVDQ_GATE_NONE) != (gate != nullptr)) return SVDQ_ERR_INVALID_ARG;
   if ((post == SVDQ_NORM_NONE && post_weight) || (pre == SVDQ_NORM_NONE && pre_weight))
     return SVDQ_ERR_INVALID_ARG;
-  if (C % 8 || C > svdq::kn::MAX_C) return SVDQ_ERR_UNSUPPORTED;
+  if (C % 8 || C > svdq::kn::MAX_C || T > INT_MAX / 2) return SVDQ_ERR_UNSUPPORTED;
   if (T == 0) return SVDQ_OK;
+  // Strides of a dimension of one are not used.
+  if (T == 1) ldx = ldy = ldh = ldn = C;
+  if (n_seqs == 1) ld_gate = ld_scale = ld_shift = 0;
   if (!x || (y && !h) || (!y && !n)) return SVDQ_ERR_INVALID_ARG;
   if (!y && (h || post != SVDQ_NORM_NONE || gate || residual_scale != 1.f))
     return SVDQ_ERR_INVALID_ARG;
@@ -1214,7 +1221,7 @@ int svdq_norm_gate_residual(int dtype, const uint16_t* x, int64_t ldx, const uin
     return SVDQ_ERR_INVALID_ARG;
   const Extent vec[] = {extent(gate, n_seqs, ld_gate, 1, C, C), extent(scale, n_seqs, ld_scale, 1, C, C),
                         extent(shift, n_seqs, ld_shift, 1, C, C), extent(post_weight, 1, C, 1, C, C),
-                        extent(pre_weight, 1, C, 1, C, C)};
+                        extent(pre_weight, 1, C, 1, C, C), offsets(cu_seqlens, n_seqs)};
   for (const Extent& v : vec)
     if (v.base && ((y && may_meet(eh, v)) || (n && may_meet(en, v)))) return SVDQ_ERR_INVALID_ARG;
   DeviceInfo* d = nullptr;
@@ -1248,7 +1255,7 @@ int svdq_norm_gate_residual(int dtype, const uint16_t* x, int64_t ldx, const uin
 
 int svdq_rope_turns(const int* axes, int n_axes, double theta, double* turns) {
   if (!axes || !turns || n_axes < 1 || n_axes > svdq::kp::MAX_AXES || !std::isfinite(theta) ||
-      theta <= 0.0)
+      theta < 1.0)
     return SVDQ_ERR_INVALID_ARG;
   int R = 0;
   for (int a = 0; a < n_axes; ++a) {
@@ -1281,14 +1288,14 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
   }
   if (R > D) return SVDQ_ERR_SHAPE;
   if (D % 8 || D > svdq::kp::MAX_D || (!interleaved && R % 8) ||
-      Hq + static_cast<int64_t>(Hk) > (1 << 16))
+      Hq + static_cast<int64_t>(Hk) > (1 << 16) || T > INT_MAX / 2)
     return SVDQ_ERR_UNSUPPORTED;
   if (T == 0) return SVDQ_OK;
   const bool has_q = Hq > 0, has_k = Hk > 0;
   if (!positions || (has_q && (!q || !q_out)) || (has_k && (!k || !k_out)) ||
       (!has_q && (q || q_out || q_weight)) || (!has_k && (k || k_out || k_weight)))
     return SVDQ_ERR_INVALID_ARG;
-  if (ld_pos < n_axes) return SVDQ_ERR_SHAPE;
+  if (T > 1 && ld_pos < n_axes) return SVDQ_ERR_SHAPE;
   auto bad_strides = [&](int64_t st, int64_t sh, int H) {
     return (T > 1 && st < D) || (H > 1 && sh < D);
   };
@@ -1304,7 +1311,10 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
                  misaligned(k_out, ko_stride_t, ko_stride_h, Hk))) ||
       !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(positions, 4))
     return SVDQ_ERR_ALIGNMENT;
-  if (T == 1) q_stride_t = k_stride_t = qo_stride_t = ko_stride_t = D;   // not used
+  if (T == 1) {   // not used
+    q_stride_t = k_stride_t = qo_stride_t = ko_stride_t = D;
+    ld_pos = n_axes;
+  }
   if (Hq <= 1) q_stride_h = qo_stride_h = D;
   if (Hk <= 1) k_stride_h = ko_stride_h = D;
   const Extent eq = extent(q, T, q_stride_t, Hq, q_stride_h, D);
@@ -1385,7 +1395,9 @@ int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_s
                    int64_t o_stride_t, int64_t o_stride_h, void* workspace,
                    size_t workspace_bytes, void* stream) {
   if (dtype != SVDQ_BF16 && dtype != SVDQ_FP16) return SVDQ_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || scale <= 0.f) return SVDQ_ERR_INVALID_ARG;
+  // (finite in units of log2 too)
+  const float scale_log2 = scale * 1.44269504088896341f;
+  if (!std::isfinite(scale_log2) || !(scale > 0.f)) return SVDQ_ERR_INVALID_ARG;
   if (T < 0 || Hq < 1 || Hk < 1 || Hq % Hk || D < 1 || n_seqs < 1 || (!cu_seqlens && n_seqs != 1))
     return SVDQ_ERR_SHAPE;
   if (D % 8 || D > svdq::ka::MAX_D ||
@@ -1418,13 +1430,16 @@ int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_s
   const Extent ek = extent(k, T, k_stride_t, Hk, k_stride_h, D);
   const Extent ev = extent(v, T, v_stride_t, Hk, v_stride_h, D);
   const Extent eo = extent(out, T, o_stride_t, Hq, o_stride_h, D);
-  if (meets_itself(eo) || may_meet(eo, eq) || may_meet(eo, ek) || may_meet(eo, ev))
+  const Extent ecu = offsets(cu_seqlens, n_seqs);
+  if (meets_itself(eo) || may_meet(eo, eq) || may_meet(eo, ek) || may_meet(eo, ev) ||
+      (cu_seqlens && may_meet(eo, ecu)))
     return SVDQ_ERR_INVALID_ARG;
   if (workspace) {
     const Extent ew = {reinterpret_cast<uintptr_t>(workspace), 1, 0, 1, 0,
                        static_cast<int64_t>(workspace_bytes)};
     for (const Extent& e : {eq, ek, ev, eo})
       if (may_meet(ew, e)) return SVDQ_ERR_INVALID_ARG;
+    if (cu_seqlens && may_meet(ew, ecu)) return SVDQ_ERR_INVALID_ARG;
   }
   DeviceInfo* d = nullptr;
   if (int st = device_setup(&d)) return st;
@@ -1442,7 +1457,7 @@ int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_s
   p.cu = cu_seqlens, p.v = v, p.out = out;
   p.vst = v_stride_t, p.vsh = v_stride_h, p.ost = o_stride_t, p.osh = o_stride_h;
   p.T = T, p.S = n_seqs, p.Hq = Hq, p.group = Hq / Hk, p.D = D, p.causal = causal ? 1 : 0;
-  p.scale_log2 = scale * 1.44269504088896341f;
+  p.scale_log2 = scale_log2;
   // At most this many work items; one persistent block per SM takes them in
   // turn, or an equal share of their key tiles.
   const int64_t items = (static_cast<int64_t>(T) / ka::ITEM_ROWS + n_seqs) * Hq;

@@ -749,7 +749,7 @@ class DitBlock:
 
 def dit_block(x: torch.Tensor, w: DitBlock, modulation, positions: torch.Tensor, plan: RopePlan,
               cu_seqlens: Optional[torch.Tensor] = None, causal: bool = False) -> torch.Tensor:
-    """One block on x [T, C] bf16 on the current stream -> the new x:
+    """One block on x [T, C] bf16 on its device's current stream -> the new x:
 
         x = x + tanh(gate_attn) * norm(out(attention(rope(qkv(norm(x) (1 + scale_attn))))))
         x = x + tanh(gate_ffn) * norm(w2(silu(w1 n) * w3 n)),  n = norm(x) (1 + scale_ffn)
@@ -757,6 +757,9 @@ def dit_block(x: torch.Tensor, w: DitBlock, modulation, positions: torch.Tensor,
     modulation: (scale_attn, gate_attn, scale_ffn, gate_ffn), each [n_seqs, C];
     rows by cu_seqlens (None: one sequence).  Rows in no sequence come back
     undefined."""
+    if x.is_cuda and x.get_device() != _current_device():
+        with _on(x.get_device(), None):
+            return dit_block(x, w, modulation, positions, plan, cu_seqlens, causal)
     scale_attn, gate_attn, scale_ffn, gate_ffn = modulation
     T, H, D, eps = x.shape[0], w.heads, w.head_dim, w.eps
     _, n = norm_gate_residual(x, scale=scale_attn, pre_weight=w.attn_pre, eps=eps,

@@ -47,10 +47,12 @@ NORM_BAD = [
     ("INVALID_ARG", dict(n=2 * MB + 128)), ("INVALID_ARG", dict(n=4 * MB)),
     ("INVALID_ARG", dict(h=1 * MB, ldh=72)),                         # other rows of x
     ("SHAPE", dict(T=-1)), ("SHAPE", dict(C=0)), ("SHAPE", dict(S=0)), ("SHAPE", dict(S=2)),
-    ("SHAPE", dict(ldx=56)), ("SHAPE", dict(ldn=32)), ("SHAPE", dict(ldg=-8)),
+    ("SHAPE", dict(ldx=56)), ("SHAPE", dict(ldn=32)), ("SHAPE", dict(ldg=-8, cu=7 * MB, S=2)),
     ("UNSUPPORTED", dict(C=60)), ("UNSUPPORTED", dict(C=8200, ldx=8200, ldy=8200, ldh=8200, ldn=8200)),
     ("ALIGNMENT", dict(x=MB + 2)), ("ALIGNMENT", dict(ldy=68)), ("ALIGNMENT", dict(scale=4 * MB + 8)),
-    ("ALIGNMENT", dict(lds=68)), ("ALIGNMENT", dict(cu=MB + 2)),
+    ("ALIGNMENT", dict(lds=68, cu=7 * MB, S=2)), ("ALIGNMENT", dict(cu=MB + 2)),
+    ("INVALID_ARG", dict(cu=5 * MB + 64)), ("INVALID_ARG", dict(cu=6 * MB - 4)),   # over h, into n
+    ("UNSUPPORTED", dict(T=1 << 30)),
 ]
 
 
@@ -72,6 +74,8 @@ NORM_GOOD = [
     dict(n=None, pre=0, scale=None), dict(y=None, h=None, post=0, gate_kind=0, gate=None),
     # x, h and n side by side in the rows of one buffer
     dict(ldx=192, h=1 * MB + 128, ldh=192, n=1 * MB + 256, ldn=192),
+    # strides that step over nothing
+    dict(T=1, ldx=0, ldy=-4, ldh=3, ldn=0), dict(ldg=-8, lds=68), dict(cu=6 * MB - 8),
 ]
 
 
@@ -108,6 +112,7 @@ ROPE_BAD = [
     ("UNSUPPORTED", dict(axes=(16, 20), il=0)),          # R = 36 in halves
     ("ALIGNMENT", dict(q=MB + 2)), ("ALIGNMENT", dict(qst=196)), ("ALIGNMENT", dict(qosh=68, qost=136)),
     ("ALIGNMENT", dict(qw=8 * MB + 2)),
+    ("UNSUPPORTED", dict(T=1 << 30)),
 ]
 
 
@@ -120,8 +125,8 @@ def test_rope_refuses(svdq, status, kw):
 @pytest.mark.parametrize("kw", [
     dict(), dict(qo=1 * MB, qost=192, ko=1 * MB + 256, kost=192),            # both in place
     dict(k=None, Hk=0, ko=None), dict(q=None, Hq=0, qo=None), dict(T=1, qst=0, kst=0, qost=8),
-    dict(axes=(16, 24, 24), il=0), dict(axes=(2, 4)),
-], ids=range(7))
+    dict(axes=(16, 24, 24), il=0), dict(axes=(2, 4)), dict(T=1, ldp=0),
+], ids=range(8))
 def test_rope_takes(svdq, kw):
     assert on_device(svdq, svdq._lib.svdq_rope_qk(*rope_args(svdq, **kw)))
 
@@ -136,7 +141,7 @@ def test_rope_plan(svdq):
             svdq.RopePlan(bad, theta=256.0, head_dim=128)
     with pytest.raises(ValueError):
         svdq.RopePlan((64, 80), theta=256.0, head_dim=128)
-    for theta in (0.0, -1.0, math.nan, math.inf):
+    for theta in (0.0, -1.0, 0.999, 1e-310, math.nan, math.inf):
         with pytest.raises(svdq.SvdqError):
             svdq.RopePlan((64,), theta=theta, head_dim=128)
 
@@ -167,6 +172,8 @@ ATTN_BAD = [
     ("ALIGNMENT", dict(k=MB + 520)), ("ALIGNMENT", dict(vst=516)), ("ALIGNMENT", dict(osh=68)),
     ("ALIGNMENT", dict(cu=MB + 1)), ("ALIGNMENT", dict(ws=5 * MB + 8, ws_bytes=1 << 30)),
     ("INVALID_ARG", dict(ws=3 * MB - 16, ws_bytes=32)),      # over out
+    ("INVALID_ARG", dict(scale=3e38)), ("INVALID_ARG", dict(cu=3 * MB + 16)),
+    ("INVALID_ARG", dict(ws=5 * MB, ws_bytes=1 << 10, cu=5 * MB + 64)),
 ]
 
 

@@ -113,6 +113,24 @@ def test_dit_block(lens, causal):
     s.check_device_error()
 
 
+def test_dit_block_enters_the_device_of_its_input(monkeypatch):
+    """Called while another device is the current one: on its input's."""
+    s = H.svdq()
+    w, _, g = make_block(60)
+    x = torch.randn(40, HIDDEN, generator=g, device=DEV).to(BF)
+    mod = torch.zeros(1, 4 * HIDDEN, device=DEV, dtype=BF).chunk(4, 1)
+    pos = torch.zeros(40, 3, device=DEV, dtype=torch.int32)
+    plan = s.RopePlan((32, 48, 48), 256.0, HIDDEN // HEADS)
+    want = s.dit_block(x, w, mod, pos, plan)
+    seen, entered = [x.get_device() + 1], []
+    real, on = s._current_device, s._on
+    monkeypatch.setattr(s, "_current_device", lambda: seen.pop() if seen else real())
+    monkeypatch.setattr(s, "_on", lambda i, stream: entered.append((i, stream)) or on(i, stream))
+    assert torch.equal(s.dit_block(x, w, mod, pos, plan), want)
+    assert entered == [(x.get_device(), None)] and not seen
+    s.check_device_error()
+
+
 def test_dit_block_refuses_other_widths():
     s = H.svdq()
     w, _, _ = make_block(50)
