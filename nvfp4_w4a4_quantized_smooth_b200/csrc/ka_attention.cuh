@@ -738,8 +738,8 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (tiles > 0) {
         const int row_keys = (p.causal ? min(it.len, row + 1) : it.len) - it.ka * ROWS;   // from ka on
         float m = -INFINITY;     // reference of the row, raw units of S
-        float off = 0.f;         // -m in log2 units
-        bool big = false;        // off is too large for one fma
+        float off = 0.f;         // -m in log2 units, 0 where m is taken off first
+        bool big = false;        // m is taken off first in a row of the warp
         uint64_t sum2 = 0;       // of the weights, even and odd keys
         for (int j = 0; j < tiles; ++j) {
           ok = __all_sync(0xFFFFFFFFu, svdq_wait(s_full(slot), ns++ & 1u, SITE_SOFT_S));
@@ -785,11 +785,15 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             for (int e = 0; e < 32; e += 2)
               t[(e >> 1) & 3] = max3(t[(e >> 1) & 3], __uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1]));
           const float top = fmaxf(max3(t[0], t[1], t[2]), t[3]);
+          // The votes say whether the warp comes here; what happens to a row
+          // is decided by its own maximum, so that rows which share a warp
+          // (other queries, rows of another sequence) do not show in it.
           const bool grown = __any_sync(0xFFFFFFFFu, (top - m) * sc > RESCALE_LOG2);
           if (grown || big) {
             if (grown) {
-              const float f = top == m ? 1.f : ex2_approx_ftz((m - top) * sc);
-              m = top;
+              const float to = (top - m) * sc > RESCALE_LOG2 ? top : m;
+              const float f = to == m ? 1.f : ex2_approx_ftz((m - to) * sc);
+              m = to;
               sum2 = mul2(sum2, pk(f, f));
               if (j > 0) {
                 // O is idle here: the commit behind s_full also covers this
@@ -811,8 +815,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             // large that this would show (2^-12 and more), m is taken off
             // first.
             if (big) {
-              const float ref = m == -INFINITY ? 0.f : m;
-              off = 0.f;
+              const bool far = m != -INFINITY && fabsf(m * sc) > 4096.f;
+              const float ref = far ? m : 0.f;
+              off = far ? 0.f : off;
 #pragma unroll
               for (int c = 0; c < 4; ++c)
 #pragma unroll
