@@ -16,11 +16,15 @@
 //
 // The softmax keeps a running reference m (log2 units after the scale), sum
 // and O relative to it.  O is rescaled only when a row's maximum has grown by
-// more than 2^8 over its reference: until then the exponentials stay below
-// 2^8, which neither the fp32 sums nor the 16-bit P lose digits over (P's
-// relative rounding is the same at every exponent, fp16's range is 65504).
-// P is rounded to the input type for the tensor core (half a step, 2^-8 of
-// each weight for bf16); the sum is over the unrounded fp32 weights.
+// more than 2^8 over its reference: until then the weights stay below 2^8
+// times the reference's.  P is rounded to the input type for the tensor core;
+// the sum is over the unrounded fp32 weights.  bf16 has fp32's exponents, so
+// a weight is off by half a step (2^-8 of it) however small it is, and the
+// reference weight is 1.  fp16 ends at 65504 and loses digits below 2^-14,
+// everything at 2^-25: there the reference weight is 2^7, the largest one
+// then 2^15, and a weight is off by 2^-11 of itself or, where that is less, by
+// 2^-32 of the reference weight (with a reference of 1, 2^-25: weak keys
+// beside a strong one lost a visible share of their mass).
 //
 // Keys that a row does not attend are replaced by -inf after the product, by
 // selection, so what they hold does not matter.  Values need more, since a
@@ -67,6 +71,9 @@ constexpr uint32_t TM_O = 256;          // O of slot s at 256 + 128 s
 constexpr int MIN_RUN = 6;               // places of a block's run, at least (split)
 constexpr int P_STEPS = 6;              // 16-key steps of P that are handed over first
 constexpr float RESCALE_LOG2 = 8.f;
+// Of the weight of a key that scores a row's reference.
+template <bool BF16>
+constexpr float REF_LOG2 = BF16 ? 0.f : 7.f;
 // Registers per thread of the softmax warps and of the others: all that the
 // block has (384 x 168).  At 4352 x 30 heads 237 us, 250 with 216 / 72 or
 // 224 / 56.
@@ -738,7 +745,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
       if (tiles > 0) {
         const int row_keys = (p.causal ? min(it.len, row + 1) : it.len) - it.ka * ROWS;   // from ka on
         float m = -INFINITY;     // reference of the row, raw units of S
-        float off = 0.f;         // -m in log2 units, 0 where m is taken off first
+        float off = REF_LOG2<BF16>;   // less m in log2 units, unless m is taken off first
         bool big = false;        // m is taken off first in a row of the warp
         uint64_t sum2 = 0;       // of the weights, even and odd keys
         for (int j = 0; j < tiles; ++j) {
@@ -807,8 +814,9 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
                   tmem_st_32x32b_x16(tm_o + c, o);
                 }
               }
-              off = m == -INFINITY ? 0.f : -m * sc;
-              big = __any_sync(0xFFFFFFFFu, fabsf(off) > 4096.f);
+              const float msc = m == -INFINITY ? 0.f : m * sc;
+              off = REF_LOG2<BF16> - msc;
+              big = __any_sync(0xFFFFFFFFu, fabsf(msc) > 4096.f);
             }
             // Exponents x sc - m sc come from one fma: the rounding of m sc,
             // 2^-24 of it, adds to the one S has anyway.  Where m sc is so
@@ -817,7 +825,7 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
             if (big) {
               const bool far = m != -INFINITY && fabsf(m * sc) > 4096.f;
               const float ref = far ? m : 0.f;
-              off = far ? 0.f : off;
+              off = far ? REF_LOG2<BF16> : off;
 #pragma unroll
               for (int c = 0; c < 4; ++c)
 #pragma unroll
