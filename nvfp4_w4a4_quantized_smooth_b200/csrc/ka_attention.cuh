@@ -271,7 +271,8 @@ struct Items {
     return r2 % n;
   }
   // Where a run begins that should begin at w: at an item's edge where one is
-  // near (two partial results less).
+  // near (two partial results less).  So no run begins at an item's last key
+  // tile, and every part has one for each row of the item.
   __device__ __forceinline__ int edge(const Params& p, int w, int total, int run) {
     if (w >= total) return total;
     if (p.S > 32) s0 = -32, next_base = front = 0;   // from the first group on again
@@ -938,10 +939,6 @@ __global__ void __launch_bounds__(NUM_THREADS, 1)
           __syncwarp();
         }
         tc_fence_before();
-      } else if (!whole && it.q0 + slot * ROWS < it.len) {
-        // (causal, the item's last key tile alone: nothing for slot 0)
-        p.ws.ml[(2 * blockIdx.x + (it.ka > 0 ? 0 : 1)) * ITEM_ROWS + slot * ROWS + r] =
-            make_float2(-INFINITY, 0.f);
       }
       if (p.causal) {
         // (also a slot that had nothing here waits for the notes: else it
@@ -1010,8 +1007,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) join_kernel(const Params p) {
       const float2 ml = p.ws.ml[place(k) + i];
       const float f = ml.x == top[i] ? 1.f : ex2_approx_ftz((ml.x - top[i]) * p.scale_log2);
       l[i] = fmaf(ml.y, f, l[i]);
-      // (a part without a key for the row has written no O)
-      if (ml.x != -INFINITY && col < dp) {
+      if (col < dp) {
         const float4 v = *reinterpret_cast<const float4*>(p.ws.o + (place(k) + i) * dp + col);
         o[i].x = fmaf(v.x, f, o[i].x);
         o[i].y = fmaf(v.y, f, o[i].y);
