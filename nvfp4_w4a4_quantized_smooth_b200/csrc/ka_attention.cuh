@@ -174,7 +174,8 @@ struct Item {
 // equal.)  Split: the items of all
 // sequences lie in one line, each as long as its key tiles and one place more
 // for what an item costs by itself, and the line is cut into equal runs, one
-// per block.  (The host keeps the places below 2^31.)
+// per block.  (The host keeps the places below 2^31 and divides calls of at
+// most 32 sequences, one group, in which places may be looked up in any order.)
 template <bool SPLIT>
 struct Items {
   int s0 = -32;                   // the present group of 32 sequences, one per lane:
@@ -241,8 +242,8 @@ struct Items {
     begin_ = __shfl_sync(0xFFFFFFFFu, begin_, from);
     len_ = __shfl_sync(0xFFFFFFFFu, len_, from);
   }
-  // The sequence that holds place w (which must not fall from call to call):
-  // the place within it, -1 behind the last.
+  // The sequence that holds place w (which must not fall to an earlier group
+  // from call to call): the place within it, -1 behind the last.
   __device__ __forceinline__ int find(const Params& p, int w, Item& it) {
     while (w >= next_base)
       if (!next_group(p)) return -1;
@@ -275,7 +276,6 @@ struct Items {
   // tile, and every part has one for each row of the item.
   __device__ __forceinline__ int edge(const Params& p, int w, int total, int run) {
     if (w >= total) return total;
-    if (p.S > 32) s0 = -32, next_base = front = 0;   // from the first group on again
     Item it;
     const int r = locate(p, w, it), n = it.all_tiles(p.causal) + 1;
     const int near = 1 + max(1, run / 16);
@@ -283,14 +283,12 @@ struct Items {
   }
   __device__ __forceinline__ void start(const Params& p) {
     if (!SPLIT) return;
-    while (next_group(p)) {
-    }
+    next_group(p);   // the only one
     const int total = next_base;
     const int run = max(MIN_RUN, (total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x));
     const int64_t w = static_cast<int64_t>(blockIdx.x) * run;
     end = edge(p, static_cast<int>(min(w + run, static_cast<int64_t>(total))), total, run);
     at = edge(p, static_cast<int>(min(w, static_cast<int64_t>(total))), total, run);
-    if (p.S > 32) s0 = -32, next_base = front = 0;
   }
   __device__ __forceinline__ bool get(const Params& p, Item& it) {
     if (SPLIT) {

@@ -1168,7 +1168,9 @@ bool ka_may_split(DeviceInfo* d, int T, int n_seqs, int Hq, int causal) {
   if (items >= d->num_sms) return false;
   const int64_t tiles = T / n_seqs / ka::ROWS;                   // of a usual sequence's longest item
   const int64_t share = items * (causal ? 1 : 2);                // twice the SMs' worth of work
-  return items * (T / ka::ROWS + 2) < INT_MAX &&
+  // More than 18 tiles a sequence in fewer items than SMs: n_seqs is below an
+  // eighth of the SMs, and the walk's one group of 32 holds them.
+  return n_seqs <= 32 && items * (T / ka::ROWS + 2) < INT_MAX &&
          tiles * (2 * d->num_sms - share) > 2 * 18 * d->num_sms;
 }
 
