@@ -86,17 +86,6 @@ __device__ __forceinline__ uint4 pack4x2(const uint64_t (&f)[4]) {
   return make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-// 16 bytes that this kernel reads once (not kept in L1).  Plain loads, not
-// the read-only path: the buffer may be the output's.
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p)
-               : "memory");
-  return v;
-}
-
 // A truth value as an argument's type.
 template <bool B>
 struct Tag {
