@@ -38,9 +38,10 @@ struct DeviceInfo {
   int ks_clusters[9];
   // Max co-resident CTA pairs of the pair GEMM; -1 = not queried yet.
   int kg2_pairs = -1;
-  // The kernels between the linears have been given their shared memory, and
-  // the attention kernels have the registers their warp roles share out.
-  bool block_ready = false;
+  // The kernels of each operator between the linears have been given their
+  // shared memory (and the attention's have the registers their warp roles
+  // share out).
+  bool norm_ready = false, rope_ready = false, attention_ready = false;
 };
 
 std::mutex g_mu;
@@ -1124,10 +1125,15 @@ int prepare_ka() {
 }
 
 template <bool BF16, int VPT>
-int prepare_kn() {
+bool prepare_kn_instance() {
   using namespace svdq::kn;
   return cudaFuncSetAttribute(norm_gate_kernel<BF16, VPT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              ring_bytes(VPT * 8 * (VPT == 1 ? 256 : MAX_THREADS), true)) == cudaSuccess
+                              ring_bytes(VPT * 8 * (VPT == 1 ? 256 : MAX_THREADS), true)) == cudaSuccess;
+}
+
+int prepare_kn() {
+  return prepare_kn_instance<true, 1>() && prepare_kn_instance<true, 2>() &&
+                 prepare_kn_instance<false, 1>() && prepare_kn_instance<false, 2>()
              ? SVDQ_OK
              : SVDQ_ERR_CUDA;
 }
@@ -1142,17 +1148,13 @@ int prepare_kp() {
   return SVDQ_OK;
 }
 
-int block_setup(DeviceInfo* d) {
+// An operator's setup, once per device.  Each has its own: what one of them
+// lacks is no matter to the others.
+int setup_once(bool* ready, int (*prepare)()) {
   std::lock_guard<std::mutex> lock(g_mu);
-  if (d->block_ready) return SVDQ_OK;
-  int st = prepare_kp();
-  if (!st) st = prepare_kn<true, 1>();
-  if (!st) st = prepare_kn<true, 2>();
-  if (!st) st = prepare_kn<false, 1>();
-  if (!st) st = prepare_kn<false, 2>();
-  if (!st) st = prepare_ka();
-  if (st) return st;
-  d->block_ready = true;
+  if (*ready) return SVDQ_OK;
+  if (int st = prepare()) return st;
+  *ready = true;
   return SVDQ_OK;
 }
 
@@ -1228,7 +1230,7 @@ int svdq_norm_gate_residual(int dtype, const uint16_t* x, int64_t ldx, const uin
     if (v.base && ((y && may_meet(eh, v)) || (n && may_meet(en, v)))) return SVDQ_ERR_INVALID_ARG;
   DeviceInfo* d = nullptr;
   if (int st = device_setup(&d)) return st;
-  if (int st = block_setup(d)) return st;
+  if (int st = setup_once(&d->norm_ready, prepare_kn)) return st;
 
   svdq::kn::Params p;
   p.x = x, p.y = y, p.gate = gate, p.scale = scale, p.shift = shift;
@@ -1334,7 +1336,7 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
       return SVDQ_ERR_INVALID_ARG;
   DeviceInfo* d = nullptr;
   if (int st = device_setup(&d)) return st;
-  if (int st = block_setup(d)) return st;
+  if (int st = setup_once(&d->rope_ready, prepare_kp)) return st;
 
   svdq::kp::Params p;
   std::memset(&p, 0, sizeof(p));
@@ -1445,7 +1447,7 @@ int svdq_attention(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_s
   }
   DeviceInfo* d = nullptr;
   if (int st = device_setup(&d)) return st;
-  if (int st = block_setup(d)) return st;
+  if (int st = setup_once(&d->attention_ready, prepare_ka)) return st;
 
   namespace ka = svdq::ka;
   const CUtensorMapDataType dt =
