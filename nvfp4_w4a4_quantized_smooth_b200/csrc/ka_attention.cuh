@@ -39,12 +39,20 @@
 // (D = 128) and the special function units 2048 cycles of exponentials; a
 // slot's tile is a chain of both (about 1350 cycles from S to P, 1500 from P
 // to the next S), so two slots in turns need about 2800.  At 4352 rows x 30
-// heads of 128: 240 us in short runs (1210 TFLOP/s, 73% of what a cuBLAS
-// product of 8192^3 reaches), 285 us in runs of a second, where the GPU is at
-// its power limit and lowers the clock (cuBLAS then: 1403 TFLOP/s).  What was
+// heads of 128: 280 us a call in runs of a second (1040 TFLOP/s, 62% of what a
+// cuBLAS product of 8192^3 reaches alone), where the GPU is at its power limit
+// and lowers the clock (cuBLAS then: 1403 TFLOP/s); 241 us in runs of some
+// milliseconds.  What was
 // tried against that: exponentials by a polynomial on the FMA units (1/8 of
 // them: 307 us, more: slower still), handing over half of P first (286 against
 // 250), five stages of the ring (1083 us against 974 at four times the rows).
+//
+// The outline is that of published work: the running maximum and sum of a
+// softmax (Milakov and Gimelshein, 2018), both products tile by tile on the
+// chip around it (Rabe and Staats, 2021; Dao et al., 2022), and for this
+// GPU's tensor memory two query tiles in turns with rescaling only where a
+// maximum has grown much.  The walk over the work items, the guard, the turns
+// and the join are this file's own.
 #pragma once
 
 #include <climits>
@@ -75,8 +83,8 @@ constexpr float RESCALE_LOG2 = 8.f;
 template <bool BF16>
 constexpr float REF_LOG2 = BF16 ? 0.f : 7.f;
 // Registers per thread of the softmax warps and of the others: all that the
-// block has (384 x 168).  At 4352 x 30 heads 237 us, 250 with 216 / 72 or
-// 224 / 56.
+// block has (384 x 168).  At 4352 x 30 heads, in short runs, 237 us, 250 with
+// 216 / 72 or 224 / 56.
 constexpr int SOFTMAX_REGS = 208, OTHER_REGS = 88;
 
 // NB: 64-element boxes per row (1: D <= 64, 2: D <= 128).

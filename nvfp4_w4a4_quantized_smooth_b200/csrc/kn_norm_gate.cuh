@@ -17,10 +17,11 @@
 // by bulk copies into a ring in shared memory, four rows ahead, which takes
 // no registers and no load instructions; the statistics of a row's branch
 // are summed together with those of the previous row's h, so that a row
-// costs one block barrier.  4352 rows x 3840 (134 MB): 26.3 us, 5.1 TB/s; 17408
-// rows with layer norm (two barriers a row): 95 us, 5.6 TB/s, 87% of a plain
-// copy's rate.  Loads one row ahead into registers took 29.6 us, a warp per row
-// (no barrier, but 255 registers and spills) 38.
+// costs one block barrier.  Calls in a row: 4352 rows x 3840 (134 MB) 27.0 us, 4.95
+// TB/s, 77% of a plain copy's rate; 17408 rows with layer norm (two barriers a
+// row) 98-99 us, 5.4 TB/s, 84%; as a graph 24.8 and 95 us.  In short runs, 26.3 us
+// then: loads one row ahead into registers 29.6 us, a warp per row (no barrier,
+// but 255 registers and spills) 38.
 #pragma once
 
 #include <cstdint>

@@ -17,11 +17,17 @@
 // with the norm's weights into sixteen registers for all heads of a unit.
 // Angles are taken in turns in 64 bits and reduced there before the 32-bit
 // sine and cosine, so a position of any int32 value keeps an angle error
-// below 2^-22 turns.  4352 tokens x 60 heads of 128 (134 MB): 28.9 us, 4.6 TB/s;
-// 9973 tokens x 40 heads in halves (204 MB): 40.9 us, 5.0 TB/s.  Issue slots
-// are 60% taken; a block per few tokens with a barrier for the angles took
-// 32.6 us, one with the whole block on a shared ring 34.1 (warps waiting for
-// the two that compute angles).
+// below 2^-22 turns.  Calls in a row: 4352 tokens x 60 heads of 128 (134 MB) 29.8
+// us, 4.5 TB/s, 69% of a plain copy's rate; 9973 tokens x 40 heads in halves (204
+// MB) 41.8 us, 4.9 TB/s, 76%; as a graph 28.2 and 40.5 us, one token 4.5.  Issue
+// slots are 60% taken.  Three blocks an SM leave 80 registers a thread; ten of
+// the twelve instances spill 4 to 20 bytes there (pairs of 128 and less 12,
+// halves 20).  In short runs, 28.9 us then: a block per few tokens with a
+// barrier for the angles 32.6 us, one with the whole block on a shared ring
+// 34.1 (warps waiting for the two that compute angles), packed two-wide
+// arithmetic 29.6 (half the instructions, at half the rate), units of 2 KB in
+// rings of four 33.2; four passes unrolled gain 1.5% here and lose 3% at 17408
+// tokens.
 #pragma once
 
 #include <cstdint>

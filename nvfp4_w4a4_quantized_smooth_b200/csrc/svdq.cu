@@ -1162,8 +1162,12 @@ int setup_once(bool* ready, int (*prepare)()) {
 // fewer than the SMs and a run of an equal share is shorter than the longest
 // item by more than dividing and joining cost, about 18 key tiles' time.
 // (Measured with one sequence, divided against whole, D = 128: full, 8192
-// rows x 2 heads 70 us / 102 us, 4352 x 4 53 / 58, 4352 x 8 80 / 60; causal,
-// 16384 x 1 99 / 201, 8192 x 4 100 / 110, 2304 x 14 57 / 43.)
+// rows x 2 heads 67 us / 119 us, 4352 x 4 49 / 61, 3000 x 1 29 / 44, 4352 x 8
+// 80 / 60; causal, 16384 x 1 80-100 / 205, 8192 x 4 82 / 112, 2304 x 14 57 / 43.
+// D = 64: full, 8192 x 2 60 / 99, 4352 x 4 41 / 55, 3000 x 1 25 / 40; causal,
+// 16384 x 1 64 / 192, 8192 x 4 66 / 100.)  The host does not see the offsets: the
+// sequences' mean length stands for the longest, so one long sequence beside
+// many short ones may be left whole.
 bool ka_may_split(DeviceInfo* d, int T, int n_seqs, int Hq, int causal) {
   namespace ka = svdq::ka;
   const int64_t items = (static_cast<int64_t>(T) + ka::ITEM_ROWS - 1) / ka::ITEM_ROWS * Hq;

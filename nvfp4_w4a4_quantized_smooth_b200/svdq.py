@@ -762,7 +762,7 @@ def dit_block(x: torch.Tensor, w: DitBlock, modulation, positions: torch.Tensor,
 
     modulation: (scale_attn, gate_attn, scale_ffn, gate_ffn), each [n_seqs, C];
     rows by cu_seqlens (None: one sequence).  Rows in no sequence come back
-    undefined."""
+    undefined and reach no other row.  T >= 1, as for the linears."""
     if x.is_cuda and x.get_device() != _current_device():
         with _on(x.get_device(), None):
             return dit_block(x, w, modulation, positions, plan, cu_seqlens, causal)
