@@ -383,7 +383,9 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
  * j over all L rows (causal = 0) or j <= i; query head h uses key / value
  * head h / (Hq / Hk).  Scores, softmax and sums in fp32; the weights are
  * rounded to the tensors' type for the product with v (fp16: to half a step,
- * or to 2^-32 of the row's largest where that is more).  Keys and values that
+ * or to 2^-32 of the row's largest where that is more).  The tensor core cuts
+ * its fp32 sums off: values of one sign come out smaller by up to 2^-27 of
+ * themselves per key (half a step of fp16 at 65536 keys).  Keys and values that
  * a row does not attend, whatever they hold (inf, NaN), do not reach it, and
  * neither do other rows' queries: not a bit of its result depends on them.
  *   q [T, Hq, D], k, v [T, Hk, D], out [T, Hq, D]  by strides (token, head).

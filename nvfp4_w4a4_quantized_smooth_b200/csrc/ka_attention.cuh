@@ -24,7 +24,10 @@
 // everything at 2^-25: there the reference weight is 2^7, the largest one
 // then 2^15, and a weight is off by 2^-11 of itself or, where that is less, by
 // 2^-32 of the reference weight (with a reference of 1, 2^-25: weak keys
-// beside a strong one lost a visible share of their mass).
+// beside a strong one lost a visible share of their mass).  The tensor core
+// cuts O off at fp32's last place once per 16 keys, where the sum of the
+// weights is rounded: values of one sign lose up to 2^-27 per key (measured at
+// 65536 keys 0.0004, at 262144 0.0017).
 //
 // Keys that a row does not attend are replaced by -inf after the product, by
 // selection, so what they hold does not matter.  Values need more, since a
