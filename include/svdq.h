@@ -393,7 +393,7 @@ int svdq_rope_qk(int dtype, const uint16_t* q, int64_t q_stride_t, int64_t q_str
  *   workspace     NULL, or at least svdq_attention_workspace_bytes(...) bytes
  *                 (for this call's arguments, on this device; 0: none is of
  *                 use), 16-byte aligned, overwritten.  With it, where rows
- *                 are too few to fill the device (judged by T, Hq and the
+ *                 are too few to fill the device (by T, Hq and the
  *                 sequences' mean length), the key tiles are divided
  *                 among the SMs and the parts joined by a second kernel, in a
  *                 fixed order.  Results repeat bit for bit for the same call
